@@ -14,7 +14,9 @@
 #include <vector>
 
 #include "kvq_append.cuh"
+#include "kvq_chunk.cuh"
 #include "kvq_decode.cuh"
+#include "kvq_fork.cuh"
 
 struct kvq_cache {
   kvq_config cfg;                 // k_bits / v_bits / k_axis point at the vectors below
@@ -41,6 +43,7 @@ struct kvq_cache {
   std::vector<std::vector<int32_t>> free_pages;  // per layer: free page ids (a stack)
   std::vector<int32_t> pt_host;                  // [num_layers][max_batch][max_pages] mirror
   std::vector<int32_t> pages_held;               // [num_layers][max_batch]
+  std::vector<int32_t> page_refs;                // [num_layers][pool_pages] sequences that hold each page
 };
 
 namespace {
@@ -279,6 +282,7 @@ kvq_status take_pages(kvq_cache* c, int layer, const int32_t* blocks_after, int 
     while (held[b] < want && e == cudaSuccess) {
       const int32_t page = pool.back();
       pool.pop_back();
+      c->page_refs[(size_t)layer * cfg.pool_pages + page] = 1;
       row[held[b]] = page;
       u->idx[u->n] = b * c->max_pages + held[b];
       u->page[u->n] = page;
@@ -297,6 +301,17 @@ kvq_status take_pages(kvq_cache* c, int layer, const int32_t* blocks_after, int 
   delete u;
   if (e != cudaSuccess) return cuda_fail(e, "page-table update");
   return KVQ_OK;
+}
+
+// Paged caches: sequence `seq` of `layer` lets go of its pages; those no other
+// sequence holds return to the pool.
+void release_pages(kvq_cache* c, int layer, int seq) {
+  const size_t i = (size_t)layer * c->cfg.max_batch + seq;
+  const int32_t* row = &c->pt_host[i * c->max_pages];
+  int32_t* refs = &c->page_refs[(size_t)layer * c->cfg.pool_pages];
+  for (int32_t k = c->pages_held[i] - 1; k >= 0; --k)
+    if (--refs[row[k]] == 0) c->free_pages[layer].push_back(row[k]);
+  c->pages_held[i] = 0;
 }
 
 // Key or value blocks that a ring holding n of its R slots flushes when T
@@ -427,6 +442,132 @@ void plan_cta_starts(kvq::DecodeParams& p, int batch, int hkv, int64_t max_ctas,
   p.cta_start[N] = (int32_t)T;
 }
 
+// The new-operator checks: the current device holds the cache; a window of at
+// least one token.
+kvq_status check_device(const kvq_cache* c) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (dev != c->device)
+    return fail(KVQ_ERR_INVALID_ARG, "the current device %d is not the cache's device %d", dev, c->device);
+  return KVQ_OK;
+}
+kvq_status check_window(const kvq_cache* c, int32_t window) {
+  if (!c) return fail(KVQ_ERR_INVALID_ARG, "cache is null");
+  if (window < 1) return fail(KVQ_ERR_INVALID_ARG, "window %d < 1", window);
+  return check_device(c);
+}
+
+// kvq_fork_sequence after its argument checks.
+kvq_status enqueue_fork(kvq_cache* c, int src, const int32_t* dsts, int nd, cudaStream_t stream) {
+  const kvq_config& cfg = c->cfg;
+  const int P = cfg.page_blocks, G = cfg.group_k;
+  if (P > 0) {
+    // let go of the destinations' pages layer by layer, counting what returns
+    // to each pool; a pool that stays short undoes all of it
+    auto row_of = [&](int l, int d) { return &c->pt_host[((size_t)l * cfg.max_batch + d) * c->max_pages]; };
+    for (int l = 0; l < cfg.num_layers; ++l) {
+      const size_t base = (size_t)l * cfg.max_batch;
+      int32_t* refs = &c->page_refs[(size_t)l * cfg.pool_pages];
+      int64_t have = (int64_t)c->free_pages[l].size();
+      for (int i = 0; i < nd; ++i)
+        for (int k = 0; k < c->pages_held[base + dsts[i]]; ++k)
+          if (--refs[row_of(l, dsts[i])[k]] == 0) ++have;
+      const int blocks = std::max(c->q_len[base + src], c->qv_len[base + src]) / G;
+      if (blocks % P != 0 && have < nd) {
+        for (int u = 0; u <= l; ++u)
+          for (int i = 0; i < nd; ++i)
+            for (int k = 0; k < c->pages_held[(size_t)u * cfg.max_batch + dsts[i]]; ++k)
+              ++c->page_refs[(size_t)u * cfg.pool_pages + row_of(u, dsts[i])[k]];
+        return fail(KVQ_ERR_CAPACITY, "layer %d: the fork needs %d pages; the pool would have %lld free of %d", l, nd,
+                    (long long)have, cfg.pool_pages);
+      }
+    }
+    for (int l = 0; l < cfg.num_layers; ++l) {
+      const size_t base = (size_t)l * cfg.max_batch;
+      int32_t* refs = &c->page_refs[(size_t)l * cfg.pool_pages];
+      for (int i = 0; i < nd; ++i) {  // the counts are down already: a page at zero returns once
+        const int32_t* row = row_of(l, dsts[i]);
+        for (int k = c->pages_held[base + dsts[i]] - 1; k >= 0; --k)
+          if (refs[row[k]] == 0) {
+            refs[row[k]] = -1;
+            c->free_pages[l].push_back(row[k]);
+          }
+        c->pages_held[base + dsts[i]] = 0;
+      }
+      const int blocks = std::max(c->q_len[base + src], c->qv_len[base + src]) / G;
+      const int full = blocks / P, held = (blocks + P - 1) / P;
+      const int32_t* from = row_of(l, src);
+      for (int i = 0; i < nd; ++i) {
+        int32_t* row = row_of(l, dsts[i]);
+        for (int k = 0; k < full; ++k) {
+          row[k] = from[k];
+          ++refs[from[k]];
+        }
+        if (held > full) {
+          row[full] = c->free_pages[l].back();
+          c->free_pages[l].pop_back();
+          refs[row[full]] = 1;
+        }
+        c->pages_held[base + dsts[i]] = held;
+      }
+    }
+  }
+  for (int l = 0; l < cfg.num_layers; ++l) {
+    const size_t base = (size_t)l * cfg.max_batch;
+    for (int i = 0; i < nd; ++i) {
+      c->q_len[base + dsts[i]] = c->q_len[base + src];
+      c->n_len[base + dsts[i]] = c->n_len[base + src];
+      c->s_len[base + dsts[i]] = c->s_len[base + src];
+      c->qv_len[base + dsts[i]] = c->qv_len[base + src];
+    }
+  }
+  thread_local kvq::ForkParams params;  // large tables: one per thread, not on the stack
+  kvq::ForkParams& p = params;
+  p.src = src;
+  p.num_kv_heads = cfg.num_kv_heads;
+  p.page_blocks = P;
+  p.max_pages = c->max_pages;
+  for (int l0 = 0; l0 < cfg.num_layers; l0 += kvq::kForkLayers) {
+    p.layers = std::min(kvq::kForkLayers, cfg.num_layers - l0);
+    for (int i0 = 0; i0 < nd; i0 += kvq::kForkDsts) {
+      p.num_dsts = std::min(kvq::kForkDsts, nd - i0);
+      for (int i = 0; i < p.num_dsts; ++i) p.dst[i] = dsts[i0 + i];
+      for (int e = 0; e < p.layers; ++e) {
+        const kvq::LayerView v = layer_view(c, l0 + e);
+        const size_t at = (size_t)(l0 + e) * cfg.max_batch + src;
+        kvq::ForkLayer& f = p.layer[e];
+        f.blocks = v.blocks;
+        f.ring_k = v.ring_k;
+        f.ring_v = v.ring_v;
+        f.sink_k = v.sink_k;
+        f.sink_v = v.sink_v;
+        f.lens = v.lens;
+        f.page_table = const_cast<int32_t*>(v.page_table);
+        const int64_t seq_ring = (int64_t)cfg.num_kv_heads * kvq::kHeadDim * 2;  // bytes of one ring slot, all heads
+        f.ring_k_bytes = seq_ring * v.residual;
+        f.ring_v_bytes = seq_ring * v.residual_v;
+        f.sink_bytes = cfg.sink_tokens > 0 ? seq_ring * KVQ_MAX_SINKS : 0;
+        const int blocks = std::max(c->q_len[at], c->qv_len[at]) / G;
+        // contiguous: each head's records; paged: the records of each head in the last, partly filled page
+        f.head_bytes = (int64_t)(P > 0 ? blocks % P : blocks) * v.record_bytes;
+        f.head_stride = (P > 0 ? P : v.max_blocks) * v.record_bytes;
+        f.full_pages = P > 0 ? blocks / P : 0;
+        f.tail_src = 0;
+        if (P > 0 && blocks % P != 0) {
+          f.tail_src = c->pt_host[at * c->max_pages + f.full_pages];
+          for (int i = 0; i < p.num_dsts; ++i)
+            p.tail_dst[e][i] = c->pt_host[((size_t)(l0 + e) * cfg.max_batch + p.dst[i]) * c->max_pages + f.full_pages];
+        }
+      }
+      const cudaError_t e = kvq::launch_fork(p, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "fork launch");
+      ++c->launches;
+    }
+  }
+  return KVQ_OK;
+}
+
 }  // namespace
 
 namespace kvq {
@@ -441,7 +582,7 @@ namespace kvq {
 // kernel was enqueued just before.
 kvq_status enqueue_decode(kvq_cache* c, int32_t layer, const void* new_k, const void* new_v, const void* q, void* out,
                           int32_t out_dtype, float softmax_scale, int32_t batch, void* stream,
-                          const StaticScratch* scratch, const QueryGroup* qg, bool after_flush) {
+                          const StaticScratch* scratch, const QueryGroup* qg, bool after_flush, int32_t window) {
   kvq_status s = check_cache_layer(c, layer);
   if (s != KVQ_OK) return s;
   if (batch < 0 || batch > c->cfg.max_batch)
@@ -520,6 +661,7 @@ kvq_status enqueue_decode(kvq_cache* c, int32_t layer, const void* new_k, const 
   p.qtok = qtok;
   p.lag_base = qg ? qg->lag_base : 0;
   p.err = reinterpret_cast<int32_t*>(c->arena + c->err_off);
+  p.window = window;
   cudaError_t e;
   if (use_mma) {
     // Persistent plan from the host mirror: the work items of every
@@ -527,18 +669,29 @@ kvq_status enqueue_decode(kvq_cache* c, int32_t layer, const void* new_k, const 
     // concatenated and cut into one contiguous range of equal cost per CTA,
     // one CTA per resident slot (fewer if there is little work).
     const kvq::MmaPlan mp = kvq::make_mma_plan(L, Hv);
-    const int per_sm = kvq::mma_ctas_per_sm(L, mp, Hv);
+    const int per_sm = kvq::mma_ctas_per_sm(L, mp, Hv, window > 0);
+    thread_local WindowTables wt;
     for (int b = 0; b < batch; ++b) {
       const size_t i = (size_t)layer * cfg.max_batch + b;
       p.nblk[b] = c->q_len[i] / L.tile_tokens;  // tile items of the quantized blocks
       p.nres[b] = c->n_len[i];
-      p.nitem[b] = kvq::unit_items(p.nblk[b], p.nres[b], c->s_len[i]);
+      int32_t nres = p.nres[b];
+      if (window > 0) {
+        // the tiles and ring chunks below the window's first position are no items
+        const int32_t lo = std::max(0, c->q_len[i] + c->n_len[i] - window);
+        wt.lo[b] = lo;
+        wt.tile0[b] = std::min(lo, c->q_len[i]) / L.tile_tokens;
+        wt.chunk0[b] = std::max(0, lo - c->q_len[i]) / kvq::kResChunk;
+        p.nblk[b] -= wt.tile0[b];
+        nres -= wt.chunk0[b] * kvq::kResChunk;
+      }
+      p.nitem[b] = kvq::unit_items(p.nblk[b], nres, c->s_len[i]);
     }
     p.persistent = 1;
     p.slots = slot_cap;
     p.after_flush = after_flush ? 1 : 0;
     plan_cta_starts(p, batch, cfg.num_kv_heads, (int64_t)std::max(1, c->sm_count) * per_sm, slot_cap);
-    e = kvq::launch_decode_mma(p, mp, st);
+    e = kvq::launch_decode_mma(p, mp, window > 0 ? &wt : nullptr, st);
     if (e == cudaSuccess) e = kvq::launch_combine(p, st);
     if (e == cudaSuccess) c->launches += 2;  // the decode kernel and the combine
   } else {
@@ -551,7 +704,8 @@ kvq_status enqueue_decode(kvq_cache* c, int32_t layer, const void* new_k, const 
     int max_blk = 0;
     for (int b = 0; b < batch; ++b) {
       const size_t i = (size_t)layer * cfg.max_batch + b;
-      nblk[b] = std::max(c->q_len[i], c->qv_len[i]) / G;
+      nblk[b] = std::max(c->q_len[i], c->qv_len[i]) / G -
+                kvq::window_block0(window, c->q_len[i], c->n_len[i], c->qv_len[i], G);
       max_blk = std::max(max_blk, nblk[b]);
     }
     const int64_t slots_gpu = (int64_t)std::max(1, c->sm_count) * per_sm;
@@ -585,6 +739,94 @@ kvq_status report_status(kvq_status s, const char* what) { return fail(s, "%s", 
 int cache_device(const kvq_cache* c) { return c->device; }
 
 }  // namespace kvq
+
+namespace {
+
+// kvq_decode_step and its windowed form (window 0: none).
+kvq_status enqueue_step(kvq_cache* c, int32_t layer, const void* k, const void* v, const void* q, void* out,
+                        int32_t out_dtype, float softmax_scale, int32_t batch, int32_t window, void* stream) {
+  kvq_status s = check_cache_layer(c, layer);
+  if (s != KVQ_OK) return s;
+  if (batch < 0 || batch > c->cfg.max_batch)
+    return fail(KVQ_ERR_INVALID_ARG, "batch %d outside 0..%d", batch, c->cfg.max_batch);
+  if (out_dtype != KVQ_F32 && out_dtype != KVQ_F16 && out_dtype != KVQ_BF16)
+    return fail(KVQ_ERR_INVALID_ARG, "out_dtype %d", out_dtype);
+  if (!std::isfinite(softmax_scale)) return fail(KVQ_ERR_INVALID_ARG, "softmax_scale is not finite");
+  if (batch == 0) return KVQ_OK;
+  if (!k || !v || !q || !out) return fail(KVQ_ERR_INVALID_ARG, "k, v, q or out is null");
+  if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(out))
+    return fail(KVQ_ERR_INVALID_ARG, "k, v, q and out must be 16-byte aligned");
+  const kvq_config& cfg = c->cfg;
+  const size_t base = (size_t)layer * cfg.max_batch;
+  // The new tokens ride along with the decode when the layer runs on the
+  // tensor-core kernel, every sequence's sinks are complete and keys and
+  // values share one ring: the prep kernel then quantizes the oldest G
+  // tokens of every full ring (one block per such sequence and KV head),
+  // its plan counts the new tokens, and the decode kernel writes them into
+  // their ring slots. Otherwise: append, then decode.
+  bool fused = kvq::mma_supported(layer_view(c, layer), c->cfg.num_q_heads) && residual_v_of(cfg) == cfg.residual;
+  bool flush = false;
+  for (int b = 0; b < batch; ++b) {
+    const int64_t L = (int64_t)c->s_len[base + b] + c->q_len[base + b] + c->n_len[base + b] + 1;
+    if (L > cfg.max_tokens)
+      return fail(KVQ_ERR_CAPACITY, "sequence %d would hold %lld tokens > max_tokens %d", b, (long long)L,
+                  cfg.max_tokens);
+    if (c->s_len[base + b] < cfg.sink_tokens) fused = false;
+    flush = flush || c->n_len[base + b] == cfg.residual;
+  }
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!fused) {
+    thread_local std::vector<int32_t> ones;
+    ones.assign(batch, 1);
+    s = enqueue_append(c, layer, k, v, ones.data(), batch, false, st);
+    if (s != KVQ_OK) return s;
+    return kvq::enqueue_decode(c, layer, nullptr, nullptr, q, out, out_dtype, softmax_scale, batch, stream, nullptr,
+                               nullptr, false, window);
+  }
+  const int G = cfg.group_k;
+  if (flush && cfg.page_blocks > 0) {
+    thread_local std::vector<int32_t> blocks_after;
+    blocks_after.resize(batch);
+    for (int b = 0; b < batch; ++b)
+      blocks_after[b] = (c->q_len[base + b] + (c->n_len[base + b] == cfg.residual ? G : 0)) / G;
+    s = take_pages(c, layer, blocks_after.data(), batch, st);
+    if (s != KVQ_OK) return s;
+  }
+  thread_local std::vector<int32_t> flushed;
+  flushed.assign(batch, 0);
+  for (int b = 0; b < batch; ++b) {
+    if (c->n_len[base + b] == cfg.residual) {
+      flushed[b] = 1;
+      c->q_len[base + b] += G;
+      c->qv_len[base + b] += G;
+      c->n_len[base + b] -= G;
+    }
+    ++c->n_len[base + b];
+  }
+  if (flush) {
+    kvq::FlushParams fp;
+    fp.L = layer_view(c, layer);
+    fp.ctas = batch * cfg.num_kv_heads;
+    const cudaError_t e = kvq::launch_step_flush(fp, st);
+    if (e != cudaSuccess) s = cuda_fail(e, "flush launch");
+    else ++c->launches;
+  }
+  if (s == KVQ_OK)
+    s = kvq::enqueue_decode(c, layer, k, v, q, out, out_dtype, softmax_scale, batch, stream, nullptr, nullptr, flush,
+                            window);
+  if (s != KVQ_OK)
+    for (int b = 0; b < batch; ++b) {
+      --c->n_len[base + b];
+      if (flushed[b]) {
+        c->q_len[base + b] -= G;
+        c->qv_len[base + b] -= G;
+        c->n_len[base + b] += G;
+      }
+    }
+  return s;
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -654,6 +896,7 @@ kvq_status kvq_cache_create(const kvq_config* cfg, void* dev_arena, size_t arena
       for (int32_t i = cfg->pool_pages - 1; i >= 0; --i) f.push_back(i);
     c->pt_host.assign((size_t)cfg->num_layers * cfg->max_batch * c->max_pages, 0);
     c->pages_held.assign((size_t)cfg->num_layers * cfg->max_batch, 0);
+    c->page_refs.assign((size_t)cfg->num_layers * cfg->pool_pages, 0);
   }
   c->q_len.assign((size_t)cfg->num_layers * cfg->max_batch, 0);
   c->n_len.assign((size_t)cfg->num_layers * cfg->max_batch, 0);
@@ -713,6 +956,7 @@ kvq_status kvq_cache_reset(kvq_cache* c, void* stream) {
       for (int32_t i = c->cfg.pool_pages - 1; i >= 0; --i) f.push_back(i);
     }
     std::fill(c->pages_held.begin(), c->pages_held.end(), 0);
+    std::fill(c->page_refs.begin(), c->page_refs.end(), 0);
   }
   return KVQ_OK;
 }
@@ -730,11 +974,7 @@ kvq_status kvq_release_sequence(kvq_cache* c, int32_t seq, void* stream) {
   for (int l = 0; l < cfg.num_layers; ++l) {
     const size_t i = (size_t)l * cfg.max_batch + seq;
     c->q_len[i] = c->n_len[i] = c->s_len[i] = c->qv_len[i] = 0;
-    if (cfg.page_blocks > 0) {
-      const int32_t* row = &c->pt_host[i * c->max_pages];
-      for (int32_t k = c->pages_held[i] - 1; k >= 0; --k) c->free_pages[l].push_back(row[k]);
-      c->pages_held[i] = 0;
-    }
+    if (cfg.page_blocks > 0) release_pages(c, l, seq);
   }
   return KVQ_OK;
 }
@@ -827,86 +1067,121 @@ kvq_status kvq_decode_attention_multi(kvq_cache* c, int32_t layer, const void* q
   return KVQ_OK;
 }
 
-kvq_status kvq_decode_step(kvq_cache* c, int32_t layer, const void* k, const void* v, const void* q, void* out,
-                           int32_t out_dtype, float softmax_scale, int32_t batch, void* stream) {
+kvq_status kvq_chunk_attention(kvq_cache* c, int32_t layer, const void* k, const void* v, const void* q, void* out,
+                               int32_t out_dtype, float softmax_scale, const int32_t* new_lens, int32_t batch,
+                               int32_t window, void* stream) {
   g_last_error.clear();
   kvq_status s = check_cache_layer(c, layer);
   if (s != KVQ_OK) return s;
-  if (batch < 0 || batch > c->cfg.max_batch)
-    return fail(KVQ_ERR_INVALID_ARG, "batch %d outside 0..%d", batch, c->cfg.max_batch);
+  s = check_device(c);
+  if (s != KVQ_OK) return s;
+  const kvq_config& cfg = c->cfg;
+  if (batch < 0 || batch > cfg.max_batch)
+    return fail(KVQ_ERR_INVALID_ARG, "batch %d outside 0..%d", batch, cfg.max_batch);
   if (out_dtype != KVQ_F32 && out_dtype != KVQ_F16 && out_dtype != KVQ_BF16)
     return fail(KVQ_ERR_INVALID_ARG, "out_dtype %d", out_dtype);
   if (!std::isfinite(softmax_scale)) return fail(KVQ_ERR_INVALID_ARG, "softmax_scale is not finite");
-  if (batch == 0) return KVQ_OK;
+  if (window < 0) return fail(KVQ_ERR_INVALID_ARG, "window %d < 0", window);
+  if (batch > 0 && !new_lens) return fail(KVQ_ERR_INVALID_ARG, "new_lens is null");
+  int64_t total = 0;
+  for (int b = 0; b < batch; ++b) {
+    if (new_lens[b] < 0) return fail(KVQ_ERR_INVALID_ARG, "new_lens[%d] = %d < 0", b, new_lens[b]);
+    const size_t i = (size_t)layer * cfg.max_batch + b;
+    if ((int64_t)c->s_len[i] + c->q_len[i] + c->n_len[i] + new_lens[b] > (1 << 30))
+      return fail(KVQ_ERR_INVALID_ARG, "sequence %d would end past token 2^30", b);
+    total += new_lens[b];
+  }
+  if (total > INT32_MAX / 64) return fail(KVQ_ERR_INVALID_ARG, "more than %d tokens in one call", INT32_MAX / 64);
+  if (total == 0) return KVQ_OK;
   if (!k || !v || !q || !out) return fail(KVQ_ERR_INVALID_ARG, "k, v, q or out is null");
   if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(out))
     return fail(KVQ_ERR_INVALID_ARG, "k, v, q and out must be 16-byte aligned");
-  const kvq_config& cfg = c->cfg;
-  const size_t base = (size_t)layer * cfg.max_batch;
-  // The new tokens ride along with the decode when the layer runs on the
-  // tensor-core kernel, every sequence's sinks are complete and keys and
-  // values share one ring: the prep kernel then quantizes the oldest G
-  // tokens of every full ring (one block per such sequence and KV head),
-  // its plan counts the new tokens, and the decode kernel writes them into
-  // their ring slots. Otherwise: append, then decode.
-  bool fused = kvq::mma_supported(layer_view(c, layer), c->cfg.num_q_heads) && residual_v_of(cfg) == cfg.residual;
-  bool flush = false;
+  thread_local kvq::ChunkParams params;  // large (per-sequence tables): one per thread, not on the stack
+  kvq::ChunkParams& p = params;
+  p.L = layer_view(c, layer);
+  p.k = k;
+  p.v = v;
+  p.q = q;
+  p.out = out;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.out_dtype = out_dtype;
+  p.num_q_heads = cfg.num_q_heads;
+  p.window = window;
+  p.sink_tokens = cfg.sink_tokens;
+  p.nseq = 0;
+  int32_t off = 0;
   for (int b = 0; b < batch; ++b) {
-    const int64_t L = (int64_t)c->s_len[base + b] + c->q_len[base + b] + c->n_len[base + b] + 1;
-    if (L > cfg.max_tokens)
-      return fail(KVQ_ERR_CAPACITY, "sequence %d would hold %lld tokens > max_tokens %d", b, (long long)L,
-                  cfg.max_tokens);
-    if (c->s_len[base + b] < cfg.sink_tokens) fused = false;
-    flush = flush || c->n_len[base + b] == cfg.residual;
+    const size_t i = (size_t)layer * cfg.max_batch + b;
+    if (new_lens[b] > 0) {
+      const int e = p.nseq++;
+      p.seq[e] = b;
+      p.s[e] = c->s_len[i];
+      p.q_len[e] = c->q_len[i];
+      p.qv_len[e] = c->qv_len[i];
+      p.n_len[e] = c->n_len[i];
+      p.t_new[e] = new_lens[b];
+      p.in_off[e] = off;
+    }
+    off += new_lens[b];
   }
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!fused) {
-    thread_local std::vector<int32_t> ones;
-    ones.assign(batch, 1);
-    s = enqueue_append(c, layer, k, v, ones.data(), batch, false, st);
-    if (s != KVQ_OK) return s;
-    return kvq::enqueue_decode(c, layer, nullptr, nullptr, q, out, out_dtype, softmax_scale, batch, stream, nullptr);
+  int64_t items = 0;
+  const int ngr = cfg.num_q_heads / cfg.num_kv_heads;
+  for (int x = 0; x < p.nseq; ++x) {
+    p.item0[x] = (int32_t)items;
+    items += (int64_t)cfg.num_kv_heads * (((int64_t)p.t_new[x] * ngr + kvq::kChunkRows - 1) / kvq::kChunkRows);
+    if (items > INT32_MAX) return fail(KVQ_ERR_UNSUPPORTED, "too many query rows in one call");
   }
-  const int G = cfg.group_k;
-  if (flush && cfg.page_blocks > 0) {
-    thread_local std::vector<int32_t> blocks_after;
-    blocks_after.resize(batch);
-    for (int b = 0; b < batch; ++b)
-      blocks_after[b] = (c->q_len[base + b] + (c->n_len[base + b] == cfg.residual ? G : 0)) / G;
-    s = take_pages(c, layer, blocks_after.data(), batch, st);
-    if (s != KVQ_OK) return s;
+  p.items = (int32_t)items;
+  const cudaError_t e = kvq::launch_chunk_simple(p, st);
+  if (e == cudaSuccess) ++c->launches;
+  if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+  return KVQ_OK;
+}
+
+kvq_status kvq_decode_attention_window(kvq_cache* c, int32_t layer, const void* q, void* out, int32_t out_dtype,
+                                       float softmax_scale, int32_t batch, int32_t window, void* stream) {
+  g_last_error.clear();
+  kvq_status s = check_window(c, window);
+  if (s != KVQ_OK) return s;
+  return kvq::enqueue_decode(c, layer, nullptr, nullptr, q, out, out_dtype, softmax_scale, batch, stream, nullptr,
+                             nullptr, false, window);
+}
+
+kvq_status kvq_decode_step(kvq_cache* c, int32_t layer, const void* k, const void* v, const void* q, void* out,
+                           int32_t out_dtype, float softmax_scale, int32_t batch, void* stream) {
+  g_last_error.clear();
+  return enqueue_step(c, layer, k, v, q, out, out_dtype, softmax_scale, batch, 0, stream);
+}
+
+kvq_status kvq_decode_step_window(kvq_cache* c, int32_t layer, const void* k, const void* v, const void* q, void* out,
+                                  int32_t out_dtype, float softmax_scale, int32_t batch, int32_t window,
+                                  void* stream) {
+  g_last_error.clear();
+  kvq_status s = check_window(c, window);
+  if (s != KVQ_OK) return s;
+  return enqueue_step(c, layer, k, v, q, out, out_dtype, softmax_scale, batch, window, stream);
+}
+
+kvq_status kvq_fork_sequence(kvq_cache* c, int32_t src, const int32_t* dsts, int32_t num_dsts, void* stream) {
+  g_last_error.clear();
+  if (!c) return fail(KVQ_ERR_INVALID_ARG, "cache is null");
+  kvq_status s = check_device(c);
+  if (s != KVQ_OK) return s;
+  const kvq_config& cfg = c->cfg;
+  if (src < 0 || src >= cfg.max_batch) return fail(KVQ_ERR_INVALID_ARG, "src %d outside 0..%d", src, cfg.max_batch - 1);
+  if (num_dsts < 0) return fail(KVQ_ERR_INVALID_ARG, "num_dsts %d < 0", num_dsts);
+  if (num_dsts == 0) return KVQ_OK;
+  if (!dsts) return fail(KVQ_ERR_INVALID_ARG, "dsts is null");
+  bool named[KVQ_MAX_BATCH] = {};
+  for (int i = 0; i < num_dsts; ++i) {
+    const int d = dsts[i];
+    if (d < 0 || d >= cfg.max_batch) return fail(KVQ_ERR_INVALID_ARG, "dsts[%d] = %d outside 0..%d", i, d, cfg.max_batch - 1);
+    if (d == src) return fail(KVQ_ERR_INVALID_ARG, "dsts[%d] is the source %d", i, src);
+    if (named[d]) return fail(KVQ_ERR_INVALID_ARG, "dsts names sequence %d twice", d);
+    named[d] = true;
   }
-  thread_local std::vector<int32_t> flushed;
-  flushed.assign(batch, 0);
-  for (int b = 0; b < batch; ++b) {
-    if (c->n_len[base + b] == cfg.residual) {
-      flushed[b] = 1;
-      c->q_len[base + b] += G;
-      c->qv_len[base + b] += G;
-      c->n_len[base + b] -= G;
-    }
-    ++c->n_len[base + b];
-  }
-  if (flush) {
-    kvq::FlushParams fp;
-    fp.L = layer_view(c, layer);
-    fp.ctas = batch * cfg.num_kv_heads;
-    const cudaError_t e = kvq::launch_step_flush(fp, st);
-    if (e != cudaSuccess) s = cuda_fail(e, "flush launch");
-    else ++c->launches;
-  }
-  if (s == KVQ_OK)
-    s = kvq::enqueue_decode(c, layer, k, v, q, out, out_dtype, softmax_scale, batch, stream, nullptr, nullptr, flush);
-  if (s != KVQ_OK)
-    for (int b = 0; b < batch; ++b) {
-      --c->n_len[base + b];
-      if (flushed[b]) {
-        c->q_len[base + b] -= G;
-        c->qv_len[base + b] -= G;
-        c->n_len[base + b] += G;
-      }
-    }
-  return s;
+  return enqueue_fork(c, src, dsts, num_dsts, static_cast<cudaStream_t>(stream));
 }
 
 kvq_status kvq_dequant(kvq_cache* c, int32_t layer, int32_t seq, int32_t t0, int32_t t1, float* k_out,

@@ -1,0 +1,42 @@
+// Parameters and launchers of chunk attention (kvq_chunk_attention): a chunk
+// of new tokens of every sequence attends to the sequence's cached tokens and
+// causally to the chunk itself.
+#pragma once
+
+#include "kvq_internal.cuh"
+
+namespace kvq {
+
+// One launch. The tables hold the sequences that have new tokens, in launch
+// order (the host puts the longest work first); entry i is sequence seq[i].
+// Positions: cached token c of a sequence is sink c (c < s), then position
+// c - s after the sinks: a quantized token below q (keys) / qv (values), else
+// a ring token. New token t is the sequence's token len + t, len = s + q + n.
+// Query token t sees token c when c <= len + t and, with a window, when also
+// c > len + t - window or c < sink_tokens.
+struct ChunkParams {
+  LayerView L;
+  const void* k;        // [tokens][Hkv][D] kv dtype, the chunk's keys
+  const void* v;
+  const void* q;        // [tokens][Hq][D] kv dtype
+  void* out;            // [tokens][Hq][D] out dtype
+  float scale_log2;     // softmax scale * log2(e)
+  int32_t out_dtype;
+  int32_t num_q_heads;
+  int32_t window;       // 0: none
+  int32_t sink_tokens;  // S of the cache: tokens that stay visible outside the window
+  int32_t nseq;         // entries of the tables
+  int32_t items;        // work items of all entries
+  int32_t seq[KVQ_MAX_BATCH];
+  int32_t s[KVQ_MAX_BATCH], q_len[KVQ_MAX_BATCH], qv_len[KVQ_MAX_BATCH], n_len[KVQ_MAX_BATCH];  // host mirror
+  int32_t t_new[KVQ_MAX_BATCH];   // new tokens
+  int32_t in_off[KVQ_MAX_BATCH];  // first row of the sequence in k, v, q and out
+  int32_t item0[KVQ_MAX_BATCH];   // first work item
+};
+
+constexpr int kChunkRows = 16;  // query rows (token, head) of one CTA of the CUDA-core kernel
+
+// The CUDA-core kernel: every cache format.
+cudaError_t launch_chunk_simple(const ChunkParams& p, cudaStream_t stream);
+
+}  // namespace kvq

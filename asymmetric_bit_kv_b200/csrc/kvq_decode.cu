@@ -93,7 +93,9 @@ __global__ void __launch_bounds__(128) decode_split_simple_kernel(DecodeParams p
   // residual lengths for keys and values)
   const int QM = max(Q, QV), nblk = QM / G;
   const int bps = p.blocks_per_split;
-  const int S = (nblk + bps - 1) / bps;
+  const int lo = p.window > 0 ? max(0, Q + n - p.window) : 0;  // first position that is not hidden
+  const int blk0 = window_block0(p.window, Q, n, QV, G);
+  const int S = (nblk - blk0 + bps - 1) / bps;
   if (s > S) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int D = kHeadDim;
@@ -141,6 +143,7 @@ __global__ void __launch_bounds__(128) decode_split_simple_kernel(DecodeParams p
       // e < nsink: sink e; otherwise the token at position QM + e - nsink
       const bool sink = e < nsink;
       const int i = QM + e - nsink;
+      if (!sink && i < lo) continue;
       const int64_t krow = sink ? (unit * KVQ_MAX_SINKS + e) * D : (unit * R + i % R) * D;
       const int64_t vrow = sink ? (unit * KVQ_MAX_SINKS + e) * D : (unit * RV + i % RV) * D;
       const void* ksrc = sink ? L.sink_k : L.ring_k;
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(128) decode_split_simple_kernel(DecodeParams p
     const int kb = L.k_bits, Gv = L.group_v;
     const int kper = 32 / kb;
     const uint32_t kmask = (1u << kb) - 1;
-    const int j0 = (s - 1) * bps, j1 = min(s * bps, nblk);
+    const int j0 = blk0 + (s - 1) * bps, j1 = min(blk0 + s * bps, nblk);
     const int64_t unit = (int64_t)b * L.num_kv_heads + h;
     for (int j = j0; j < j1; ++j) {
       const uint8_t* rec = record_ptr(L, b, h, j);
@@ -176,6 +179,7 @@ __global__ void __launch_bounds__(128) decode_split_simple_kernel(DecodeParams p
 #pragma unroll 1
         for (int t = warp; t < G; t += 4) {
           const int i = j * G + t;
+          if (i < lo) continue;
           float kv[4], vv[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -212,6 +216,7 @@ __global__ void __launch_bounds__(128) decode_split_simple_kernel(DecodeParams p
         const int ng = D / Gv, TT = L.tile_tokens;
 #pragma unroll 2
         for (int t = warp; t < G; t += 4) {
+          if (j * G + t < lo) continue;
           float kv[4], vv[4];
           const uint8_t* tp = rec + tile_base(L, t);
           const uint32_t* kc = reinterpret_cast<const uint32_t*>(tp + L.kc_off);
@@ -252,6 +257,7 @@ __global__ void __launch_bounds__(128) decode_split_simple_kernel(DecodeParams p
       for (int hh = 0; hh < NG; ++hh) bias[hh] = sbias[0][hh] + sbias[1][hh] + sbias[2][hh] + sbias[3][hh];
       const int TT = L.tile_tokens;
       for (int t = warp; t < G; t += 4) {
+        if (j * G + t < lo) continue;
         float kcode[4], vv[4];
         const uint32_t* kc = reinterpret_cast<const uint32_t*>(rec + tile_base(L, t) + L.kc_off);
         const int tl = t % TT, kw = tl / kper, ksh = (tl % kper) * kb;
@@ -348,7 +354,8 @@ __global__ void __launch_bounds__(32 * (WPH > 4 ? WPH : 4)) combine_kernel(Combi
       S = __ldcg(p.unit_slots + b * p.num_kv_heads + h);
     } else {
       const int32_t* len = p.lens + (int64_t)b * kLensStride;
-      const int nblk = max(len[kLenQ], len[kLenQV]) / p.group_k;
+      const int nblk = max(len[kLenQ], len[kLenQV]) / p.group_k -
+                       window_block0(p.window, len[kLenQ], len[kLenN], len[kLenQV], p.group_k);
       S = (nblk + p.blocks_per_split - 1) / p.blocks_per_split + 1;
     }
   }
@@ -526,7 +533,7 @@ cudaError_t launch_combine(const DecodeParams& p, cudaStream_t stream) {
   const CombineParams cp{p.ws_o,         p.ws_ml,          p.out,           p.unit_slots,
                          p.L.lens,       p.out_dtype,      p.num_q_heads,   p.L.num_kv_heads,
                          p.slots,        p.L.group_k,      p.blocks_per_split, p.persistent, p.L.hadamard,
-                         p.q_heads,      p.q_rows};
+                         p.q_heads,      p.q_rows,         p.window};
   switch (wph) {
     case 1: return cudaLaunchKernelEx(&cfg, combine_kernel<1>, cp);
     case 2: return cudaLaunchKernelEx(&cfg, combine_kernel<2>, cp);

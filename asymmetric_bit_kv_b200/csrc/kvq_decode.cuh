@@ -55,12 +55,25 @@ struct DecodeParams {
   int32_t q_rows;       // rows of q and out per sequence
   int32_t qtok;         // query tokens of this launch
   int32_t lag_base;
+  int32_t window;       // sliding window in tokens (0: none; see WindowTables)
   int32_t nblk[KVQ_MAX_BATCH];       // quantized blocks per sequence (host mirror)
   int32_t nres[KVQ_MAX_BATCH];       // ring tokens per sequence (host mirror)
   int32_t nitem[KVQ_MAX_BATCH];      // persistent mode: work items per unit of sequence b
   int32_t seq_start[KVQ_MAX_BATCH];  // first global item (block in split mode) of sequence b
   int32_t cta_start[kMaxCtas + 1];   // persistent mode: first global item of CTA c
 };
+
+// Sliding window, persistent mode: per sequence the first position that is
+// not hidden, lo = max(0, tokens after the sinks - window), and the tiles and
+// ring chunks wholly below it, which are no work items: item j of a unit is
+// tile tile0 + j while j < nblk (the tiles left), then ring chunk
+// chunk0 + j - nblk. The windowed kernel instances take the tables as an
+// argument of their own; the others take NoWindow and compile to what they
+// were.
+struct WindowTables {
+  int32_t lo[KVQ_MAX_BATCH], tile0[KVQ_MAX_BATCH], chunk0[KVQ_MAX_BATCH];
+};
+struct NoWindow {};
 
 constexpr int kMmaConsumers = 6;   // warps per CTA of the tensor-core kernel
 constexpr int kResChunk = 8;       // ring tokens per work item, persistent mode
@@ -72,6 +85,14 @@ static_assert(KVQ_MAX_SINKS == kResChunk, "the sink rows of a unit are one exact
 __host__ __device__ inline int32_t unit_items(int32_t nblk, int32_t nres, int32_t nsink) {
   const int32_t items = nblk + (nres + kResChunk - 1) / kResChunk + (nsink > 0 ? 1 : 0);
   return items > 0 ? items : 1;
+}
+
+// First block with a token inside the window, split mode (window 0: block 0),
+// from the sequence's quantized keys, key ring tokens and quantized values.
+__host__ __device__ inline int32_t window_block0(int32_t window, int32_t q, int32_t n, int32_t qv, int32_t G) {
+  if (window <= 0) return 0;
+  const int32_t lo = q + n > window ? q + n - window : 0, most = q > qv ? q : qv;
+  return (lo < most ? lo : most) / G;
 }
 
 // Persistent mode: the CTA whose item range [starts[c], starts[c+1]) holds
@@ -124,8 +145,9 @@ struct MmaPlan {
 bool mma_supported(const LayerView& L, int num_q_heads);
 int mma_max_rows(const LayerView& L);  // query rows per KV head one tensor-core launch takes
 MmaPlan make_mma_plan(const LayerView& L, int num_q_heads);
-int mma_ctas_per_sm(const LayerView& L, const MmaPlan& mp, int num_q_heads);
-cudaError_t launch_decode_mma(const DecodeParams& p, const MmaPlan& mp, cudaStream_t stream);
+int mma_ctas_per_sm(const LayerView& L, const MmaPlan& mp, int num_q_heads, bool windowed);
+// win: the window tables of a windowed launch, else null.
+cudaError_t launch_decode_mma(const DecodeParams& p, const MmaPlan& mp, const WindowTables* win, cudaStream_t stream);
 
 // Enqueue the CUDA-core split kernel (any supported shape) and the
 // log-sum-exp combine. max_splits is the largest quantized split count of any
@@ -144,6 +166,7 @@ struct CombineParams {
   int32_t out_dtype, num_q_heads, num_kv_heads, slots, group_k, blocks_per_split, persistent;
   int32_t hadamard;  // split mode: slots >= 1 (quantized tokens) hold rotated partials
   int32_t q_heads, q_rows;  // output row of query row j of a unit: see DecodeParams
+  int32_t window;           // split mode: the first split starts at the window's first block
 };
 
 // The log-sum-exp combine of the partial slots (after the decode kernel).
@@ -165,10 +188,11 @@ struct QueryGroup {
 // launches; the partials (and the slot table) go to `scratch` when it is not
 // null; qg: a group of query tokens (null: one query token per sequence);
 // new_k/new_v: a fused decode step's new tokens; after_flush: the step's
-// flush kernel was enqueued just before.
+// flush kernel was enqueued just before; window: a sliding window (0: none).
 kvq_status enqueue_decode(kvq_cache* c, int32_t layer, const void* new_k, const void* new_v, const void* q, void* out,
                           int32_t out_dtype, float softmax_scale, int32_t batch, void* stream,
-                          const StaticScratch* scratch, const QueryGroup* qg = nullptr, bool after_flush = false);
+                          const StaticScratch* scratch, const QueryGroup* qg = nullptr, bool after_flush = false,
+                          int32_t window = 0);
 void clear_last_error();
 kvq_status report_cuda_error(cudaError_t e, const char* what);
 kvq_status report_status(kvq_status s, const char* what);

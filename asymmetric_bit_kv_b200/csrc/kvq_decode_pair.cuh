@@ -109,9 +109,10 @@ __device__ __forceinline__ void pair_prep(const uint8_t* stage, int kc_bytes, co
 // lane (g, t) reads the score of row t / 2 for token g; P.V with column n
 // carrying the probabilities of row n / 4 (every value group of the row gets
 // the same exact product), added to O at the row scale of the value codes.
-template <bool BF16, int VB>
-__device__ __forceinline__ void pair_ring_chunk(const uint8_t* stage, const uint32_t* qw, uint2* bk, int cnt, int NG,
-                                                int lane, float score_scale, const bool (&valid)[1],
+// WIN: the chunk's first `skip` tokens are hidden by the window.
+template <bool BF16, int VB, bool WIN>
+__device__ __forceinline__ void pair_ring_chunk(const uint8_t* stage, const uint32_t* qw, uint2* bk, int cnt, int skip,
+                                                int NG, int lane, float score_scale, const bool (&valid)[1],
                                                 bool& rq_ready, SoftState<1>& sst, float (&O)[8][4],
                                                 float (&Z)[1][4]) {
   using S = PairShape<VB, 1>;  // value-side constants only
@@ -151,7 +152,7 @@ __device__ __forceinline__ void pair_ring_chunk(const uint8_t* stage, const uint
   }
   // rows 8-15 are absent; row g holds token g of the chunk
   float sc[1][2];
-  sc[0][0] = g < cnt ? Dr[0] + Dr[1] : -INFINITY;
+  sc[0][0] = g < cnt && (!WIN || g >= skip) ? Dr[0] + Dr[1] : -INFINITY;
   sc[0][1] = -INFINITY;
   softmax_update<1, 1, 1, true, true>(sc, sst, valid, O, Z, lane);
   const uint32_t ph = pack_kv<BF16>(sc[0][0], 0.f);
@@ -168,7 +169,11 @@ __device__ __forceinline__ void pair_ring_chunk(const uint8_t* stage, const uint
   for (int mt2 = 0; mt2 < 8; ++mt2) {
     const int cch = mt2 / S::MT_PER_CH, P = mt2 % S::MT_PER_CH;
     const int w = (cch * S::CH_SPAN + g * S::VCPC) / 2 + P;
-    const uint32_t x = V32[(2 * t) * 64 + w], y = V32[(2 * t + 1) * 64 + w];
+    uint32_t x = V32[(2 * t) * 64 + w], y = V32[(2 * t + 1) * 64 + w];
+    if constexpr (WIN) {  // 0 times what a hidden token holds must not reach the sums
+      if (2 * t < skip) x = 0u;
+      if (2 * t + 1 < skip) y = 0u;
+    }
     const uint32_t a[4] = {__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632), 0u, 0u};
     float r[4] = {0.f, 0.f, 0.f, 0.f};
     mma_kv<BF16>(r, a, bh, 0u);
@@ -181,9 +186,11 @@ __device__ __forceinline__ void pair_ring_chunk(const uint8_t* stage, const uint
   }
 }
 
-template <int VB, int NGRP>
-__global__ void __launch_bounds__(kThreads, 2) decode_pair_kernel(DecodeParams p, MmaPlan mp) {
+// W: NoWindow, or the tables of a sliding window.
+template <int VB, int NGRP, class W>
+__global__ void __launch_bounds__(kThreads, 2) decode_pair_kernel(DecodeParams p, MmaPlan mp, W win) {
   using S = PairShape<VB, NGRP>;
+  constexpr bool WIN = has_window<W>();
   constexpr int D = S::D;
   extern __shared__ __align__(128) uint8_t smem[];
   const int c = blockIdx.x;
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_pair_kernel(DecodeParams p
     for (int i = 0; i < SPW; ++i) mbar_init(full + i, 1);
     fence_mbar_init();
     for (int n = 0; n < SPW && n < nmine; ++n)
-      issue_item(p, mp, is, rs + warp + n * kNC, stages + (size_t)n * mp.stage_bytes, full + n, qbuf, NG);
+      issue_item(p, mp, win, is, rs + warp + n * kNC, stages + (size_t)n * mp.stage_bytes, full + n, qbuf, NG);
   }
   __syncwarp();
   bool failed = false;
@@ -275,6 +282,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_pair_kernel(DecodeParams p
       const int j = kb - u.start;
       if (j < nb) {
         // ============ quantized block of 32 tokens
+        // positions of the block below the window (the first block only)
+        const int skip = WIN && j == 0 ? first_seen(win, u.b) - first_tile(win, u.b) * S::TT : 0;
         uint32_t bq[4][2];
         float bias[2];
         pair_prep(stage, mp.kc_bytes, pq, NG, lane, p.score_scale, bq, bias);
@@ -312,6 +321,16 @@ __global__ void __launch_bounds__(kThreads, 2) decode_pair_kernel(DecodeParams p
             const float s = x + __shfl_xor_sync(0xffffffffu, x, 17);
             sc[jp][r] = score_lane ? fmaf(s, p.score_scale * code_unscale<2>(2 * jp + r), bias_l) : -INFINITY;
           }
+        if constexpr (WIN) {
+          if (skip > 0) {
+#pragma unroll
+            for (int jp = 0; jp < 4; ++jp)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                if (8 * (g & 3) + 2 * jp + r < skip) sc[jp][r] = -INFINITY;
+          }
+        }
+        // (the block's last token is seen, so that every row keeps a finite score)
         softmax_update<4, 1, 1, false, true>(sc, sst, valid, O, Z, lane);
         // ---- values: O += codes x (p * s), Z += ones x (p * z)
 #pragma unroll
@@ -321,7 +340,15 @@ __global__ void __launch_bounds__(kThreads, 2) decode_pair_kernel(DecodeParams p
           const uint32_t pk0 = pack_f16(sc[2 * i][0], sc[2 * i][1]), pk1 = pack_f16(sc[2 * i + 1][0], sc[2 * i + 1][1]);
           uint32_t bt = __shfl_sync(0xffffffffu, pk0, psrc), bb = __shfl_sync(0xffffffffu, pk1, psrc);
           if (!pcol) bt = bb = 0u;
-          const uint4 v4 = vsz4[(i * 4 + t) * NGRP + vgrp];  // (s, s), (s, s), (z, z), (z, z)
+          uint4 v4 = vsz4[(i * 4 + t) * NGRP + vgrp];  // (s, s), (s, s), (z, z), (z, z)
+          if constexpr (WIN) {
+            if (skip > 0) {
+              v4.x = keep_seen(v4.x, bt);
+              v4.y = keep_seen(v4.y, bb);
+              v4.z = keep_seen(v4.z, bt);
+              v4.w = keep_seen(v4.w, bb);
+            }
+          }
           const uint32_t B0 = hmul2(bt, v4.x), B1 = hmul2(bb, v4.y);
           mma_f16(Z[0], ones, hmul2(bt, v4.z), hmul2(bb, v4.w));
           const uint32_t vrow = vc_s + (16 * i + 8 * (mi & 1) + rr) * S::VRB;
@@ -343,18 +370,21 @@ __global__ void __launch_bounds__(kThreads, 2) decode_pair_kernel(DecodeParams p
         }
       } else {
         bool sink;
-        const int cnt0 = exact_chunk(p, u.b, j - nb, sink);
+        const int cnt0 = exact_chunk(p, win, u.b, j - nb, sink);
+        const int rc = first_chunk(win, u.b) + j - nb;      // ring chunk
+        const int nq = (first_tile(win, u.b) + nb) * S::TT;  // quantized tokens
+        const int skip = WIN && !sink ? first_seen(win, u.b) - nq - rc * kResChunk : 0;
         const int cnt = sink ? cnt0 : cnt0 - (p.lag_base - qrow / ngr);
-        if (p.new_k && !sink && j - nb == (p.nres[u.b] - 1) / kResChunk) store_new_token(p, u.b, u.h, nb, stage, lane);
+        if (p.new_k && !sink && rc == (p.nres[u.b] - 1) / kResChunk) store_new_token(p, u.b, u.h, nq, stage, lane);
         if (bf16)
-          pair_ring_chunk<true, VB>(stage, qw, bkw, cnt, NG, lane, p.score_scale, valid, rq_ready, sst, O, Z);
+          pair_ring_chunk<true, VB, WIN>(stage, qw, bkw, cnt, skip, NG, lane, p.score_scale, valid, rq_ready, sst, O, Z);
         else
-          pair_ring_chunk<false, VB>(stage, qw, bkw, cnt, NG, lane, p.score_scale, valid, rq_ready, sst, O, Z);
+          pair_ring_chunk<false, VB, WIN>(stage, qw, bkw, cnt, skip, NG, lane, p.score_scale, valid, rq_ready, sst, O, Z);
       }
       __syncwarp();
       if (lane == 0 && n + SPW < nmine) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        issue_item(p, mp, is, rs + warp + (n + SPW) * kNC, stages + (size_t)st * mp.stage_bytes, full + st, qbuf, NG);
+        issue_item(p, mp, win, is, rs + warp + (n + SPW) * kNC, stages + (size_t)st * mp.stage_bytes, full + st, qbuf, NG);
       }
       if (++st == SPW) {
         st = 0;
@@ -399,7 +429,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_pair_kernel(DecodeParams p
 }
 
 template <int VB, int NGRP>
-cudaError_t launch_pair_instance(const DecodeParams& p, const MmaPlan& mp, cudaStream_t stream) {
+cudaError_t launch_pair_instance(const DecodeParams& p, const MmaPlan& mp, const WindowTables* win,
+                                 cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.num_ctas);
   cfg.blockDim = dim3(kThreads);
@@ -410,12 +441,14 @@ cudaError_t launch_pair_instance(const DecodeParams& p, const MmaPlan& mp, cudaS
   attr[0].val.programmaticStreamSerializationAllowed = p.after_flush ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<VB, NGRP>, p, mp);
+  if (win) return cudaLaunchKernelEx(&cfg, decode_pair_kernel<VB, NGRP, WindowTables>, p, mp, *win);
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<VB, NGRP, NoWindow>, p, mp, NoWindow{});
 }
 
 template <int VB, int NGRP>
-const void* pair_instance_fn() {
-  return reinterpret_cast<const void*>(decode_pair_kernel<VB, NGRP>);
+const void* pair_instance_fn(bool win) {
+  return win ? reinterpret_cast<const void*>(decode_pair_kernel<VB, NGRP, WindowTables>)
+             : reinterpret_cast<const void*>(decode_pair_kernel<VB, NGRP, NoWindow>);
 }
 
 }  // namespace tc

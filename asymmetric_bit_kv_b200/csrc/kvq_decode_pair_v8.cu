@@ -4,17 +4,18 @@
 namespace kvq {
 namespace tc {
 
-cudaError_t launch_pair_v8(int ngrp, const DecodeParams& p, const MmaPlan& mp, cudaStream_t stream) {
-  if (ngrp == 1) return launch_pair_instance<8, 1>(p, mp, stream);
-  if (ngrp == 2) return launch_pair_instance<8, 2>(p, mp, stream);
-  if (ngrp == 4) return launch_pair_instance<8, 4>(p, mp, stream);
+cudaError_t launch_pair_v8(int ngrp, const DecodeParams& p, const MmaPlan& mp, const WindowTables* win,
+                           cudaStream_t stream) {
+  if (ngrp == 1) return launch_pair_instance<8, 1>(p, mp, win, stream);
+  if (ngrp == 2) return launch_pair_instance<8, 2>(p, mp, win, stream);
+  if (ngrp == 4) return launch_pair_instance<8, 4>(p, mp, win, stream);
   return cudaErrorInvalidValue;
 }
 
-const void* fn_pair_v8(int ngrp) {
-  if (ngrp == 1) return pair_instance_fn<8, 1>();
-  if (ngrp == 2) return pair_instance_fn<8, 2>();
-  if (ngrp == 4) return pair_instance_fn<8, 4>();
+const void* fn_pair_v8(int ngrp, bool win) {
+  if (ngrp == 1) return pair_instance_fn<8, 1>(win);
+  if (ngrp == 2) return pair_instance_fn<8, 2>(win);
+  if (ngrp == 4) return pair_instance_fn<8, 4>(win);
   return nullptr;
 }
 

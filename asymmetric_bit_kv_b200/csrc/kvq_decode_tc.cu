@@ -10,8 +10,8 @@ namespace kvq {
 namespace tc {
 #define KVQ_TC_DECL(K, N)                                                                                   \
   cudaError_t launch_tc_k##K##_##N(int vb, int ngrp, bool pt, const DecodeParams& p, const MmaPlan& mp,           \
-                                   cudaStream_t s);                                                              \
-  const void* fn_tc_k##K##_##N(int vb, int ngrp, bool pt);
+                                   const WindowTables* win, cudaStream_t s);                                     \
+  const void* fn_tc_k##K##_##N(int vb, int ngrp, bool pt, bool win);
 KVQ_TC_DECL(2, 1)
 KVQ_TC_DECL(2, 2)
 KVQ_TC_DECL(4, 1)
@@ -20,8 +20,9 @@ KVQ_TC_DECL(8, 1)
 KVQ_TC_DECL(8, 2)
 #undef KVQ_TC_DECL
 #define KVQ_PAIR_DECL(V)                                                                                   \
-  cudaError_t launch_pair_v##V(int ngrp, const DecodeParams& p, const MmaPlan& mp, cudaStream_t s);            \
-  const void* fn_pair_v##V(int ngrp);
+  cudaError_t launch_pair_v##V(int ngrp, const DecodeParams& p, const MmaPlan& mp, const WindowTables* win,    \
+                               cudaStream_t s);                                                                \
+  const void* fn_pair_v##V(int ngrp, bool win);
 KVQ_PAIR_DECL(2)
 KVQ_PAIR_DECL(4)
 KVQ_PAIR_DECL(8)
@@ -35,11 +36,12 @@ int key_ntiles(const LayerView& L, int num_q_heads) { return num_q_heads / L.num
 // 32-token blocks with 2-bit keys (the pair layout): decode_pair_kernel.
 bool pair_path(const LayerView& L) { return pair_layout(L.group_k, L.k_bits); }
 
-const void* instance_for(const LayerView& L, int num_q_heads) {
+const void* instance_for(const LayerView& L, int num_q_heads, bool win) {
   const int vb = L.v_bits, ng = kHeadDim / L.group_v, nkt = key_ntiles(L, num_q_heads);
-  if (pair_path(L)) return vb == 2 ? tc::fn_pair_v2(ng) : vb == 4 ? tc::fn_pair_v4(ng) : tc::fn_pair_v8(ng);
+  if (pair_path(L)) 
+    return vb == 2 ? tc::fn_pair_v2(ng, win) : vb == 4 ? tc::fn_pair_v4(ng, win) : tc::fn_pair_v8(ng, win);
 #define KVQ_TC_PICK(K, N) \
-  if (L.k_bits == K && nkt == N) return tc::fn_tc_k##K##_##N(vb, ng, L.k_axis == 1);
+  if (L.k_bits == K && nkt == N) return tc::fn_tc_k##K##_##N(vb, ng, L.k_axis == 1, win);
   KVQ_TC_PICK(2, 1) KVQ_TC_PICK(2, 2) KVQ_TC_PICK(4, 1) KVQ_TC_PICK(4, 2) KVQ_TC_PICK(8, 1) KVQ_TC_PICK(8, 2)
 #undef KVQ_TC_PICK
   return nullptr;
@@ -126,8 +128,8 @@ MmaPlan make_mma_plan(const LayerView& L, int num_q_heads) {
   return mp;
 }
 
-int mma_ctas_per_sm(const LayerView& L, const MmaPlan& mp, int num_q_heads) {
-  const void* fn = instance_for(L, num_q_heads);
+int mma_ctas_per_sm(const LayerView& L, const MmaPlan& mp, int num_q_heads, bool windowed) {
+  const void* fn = instance_for(L, num_q_heads, windowed);
   if (!fn) return 1;
   // Once per (device, instance): opt the instance in to the device's largest
   // dynamic shared memory (so that no plan can exceed what was opted in);
@@ -138,7 +140,7 @@ int mma_ctas_per_sm(const LayerView& L, const MmaPlan& mp, int num_q_heads) {
     int smem;  // -1: the opt-in record of (dev, fn)
     int n;
   };
-  static Entry memo[256];
+  static Entry memo[512];
   static int nmemo = 0;
   static std::mutex mu;
   int dev = 0, n = 0;
@@ -150,7 +152,7 @@ int mma_ctas_per_sm(const LayerView& L, const MmaPlan& mp, int num_q_heads) {
     if (memo[i].smem == mp.smem_bytes) return memo[i].n;
     if (memo[i].smem == -1) opted = true;
   }
-  if (nmemo + 2 > 256) return 1;
+  if (nmemo + 2 > 512) return 1;
   if (!opted) {
     int optin = 0;
     cudaFuncAttributes fa;
@@ -173,14 +175,14 @@ int mma_ctas_per_sm(const LayerView& L, const MmaPlan& mp, int num_q_heads) {
 
 int mma_max_rows(const LayerView& L) { return pair_path(L) ? 2 : 8; }
 
-cudaError_t launch_decode_mma(const DecodeParams& p, const MmaPlan& mp, cudaStream_t stream) {
+cudaError_t launch_decode_mma(const DecodeParams& p, const MmaPlan& mp, const WindowTables* win, cudaStream_t stream) {
   const LayerView& L = p.L;
   const int vb = L.v_bits, ng = kHeadDim / L.group_v, nkt = key_ntiles(L, p.num_q_heads);
   if (pair_path(L))
-    return vb == 2 ? tc::launch_pair_v2(ng, p, mp, stream)
-                   : vb == 4 ? tc::launch_pair_v4(ng, p, mp, stream) : tc::launch_pair_v8(ng, p, mp, stream);
+    return vb == 2 ? tc::launch_pair_v2(ng, p, mp, win, stream)
+                   : vb == 4 ? tc::launch_pair_v4(ng, p, mp, win, stream) : tc::launch_pair_v8(ng, p, mp, win, stream);
 #define KVQ_TC_GO(K, N) \
-  if (L.k_bits == K && nkt == N) return tc::launch_tc_k##K##_##N(vb, ng, L.k_axis == 1, p, mp, stream);
+  if (L.k_bits == K && nkt == N) return tc::launch_tc_k##K##_##N(vb, ng, L.k_axis == 1, p, mp, win, stream);
   KVQ_TC_GO(2, 1) KVQ_TC_GO(2, 2) KVQ_TC_GO(4, 1) KVQ_TC_GO(4, 2) KVQ_TC_GO(8, 1) KVQ_TC_GO(8, 2)
 #undef KVQ_TC_GO
   return cudaErrorInvalidValue;

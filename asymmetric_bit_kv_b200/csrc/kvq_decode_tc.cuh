@@ -46,6 +46,8 @@
 //    page_blocks blocks.
 #pragma once
 
+#include <type_traits>
+
 #include "kvq_decode.cuh"
 
 namespace kvq {
@@ -510,9 +512,10 @@ __device__ __forceinline__ void fold_remainders(float (&O)[8][4], float (&Z)[NGR
 // (ch0, ch0+1) from both tokens, paired by one byte permute; two MMAs
 // (probability high and low parts) into a scratch accumulator, added to O at
 // the row scale of the quantized blocks' value codes (2^(p-24)).
-template <bool BF16, int VB, int NGRP, int NKT>
+// WIN: the chunk's first `skip` tokens are hidden by the window.
+template <bool BF16, int VB, int NGRP, int NKT, bool WIN>
 __device__ __forceinline__ void ring_chunk(const uint8_t* stage, const uint32_t* qw, uint2* bk,
-                                           const int (&cnt)[heads_per_lane<NKT>()], int NG,
+                                           const int (&cnt)[heads_per_lane<NKT>()], int skip, int NG,
                                            int lane, float score_scale, const bool (&valid)[heads_per_lane<NKT>()],
                                            bool& rq_ready, SoftState<heads_per_lane<NKT>()>& sst, float (&O)[8][4],
                                            float (&Z)[NGRP][4]) {
@@ -567,7 +570,7 @@ __device__ __forceinline__ void ring_chunk(const uint8_t* stage, const uint32_t*
   float sc[1][2 * HPL];
 #pragma unroll
   for (int h = 0; h < HPL; ++h) {
-    sc[0][h] = g < cnt[h] ? head_score<NKT>(Dr, 0, h) : -INFINITY;
+    sc[0][h] = g < cnt[h] && (!WIN || g >= skip) ? head_score<NKT>(Dr, 0, h) : -INFINITY;
     sc[0][HPL + h] = -INFINITY;
   }
   softmax_update<1, HPL, NGRP, true>(sc, sst, valid, O, Z, lane);
@@ -590,7 +593,11 @@ __device__ __forceinline__ void ring_chunk(const uint8_t* stage, const uint32_t*
   for (int mt2 = 0; mt2 < 8; ++mt2) {
     const int cch = mt2 / S::MT_PER_CH, P = mt2 % S::MT_PER_CH;
     const int w = (cch * S::CH_SPAN + g * S::VCPC) / 2 + P;
-    const uint32_t x = V32[(2 * t) * 64 + w], y = V32[(2 * t + 1) * 64 + w];
+    uint32_t x = V32[(2 * t) * 64 + w], y = V32[(2 * t + 1) * 64 + w];
+    if constexpr (WIN) {  // 0 times what a hidden token holds must not reach the sums
+      if (2 * t < skip) x = 0u;
+      if (2 * t + 1 < skip) y = 0u;
+    }
     const uint32_t a[4] = {__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632), 0u, 0u};
     float r[4] = {0.f, 0.f, 0.f, 0.f};
     mma_kv<BF16>(r, a, bh, 0u);
@@ -706,13 +713,31 @@ __device__ __forceinline__ void unrotate_output(float (&O)[8][4], float (&Z)[NGR
   __syncwarp();
 }
 
-// Exact-token chunk r of a unit (the items after its quantized blocks): ring
-// chunk r while r < ceil(nres / kResChunk), then the sink chunk if the
+// A sequence's window (WindowTables), or none: the first tile and ring chunk
+// that are work items, and the first position that is not hidden.
+__device__ __forceinline__ int first_tile(const NoWindow&, int) { return 0; }
+__device__ __forceinline__ int first_chunk(const NoWindow&, int) { return 0; }
+__device__ __forceinline__ int first_seen(const NoWindow&, int) { return 0; }
+__device__ __forceinline__ int first_tile(const WindowTables& w, int b) { return w.tile0[b]; }
+__device__ __forceinline__ int first_chunk(const WindowTables& w, int b) { return w.chunk0[b]; }
+__device__ __forceinline__ int first_seen(const WindowTables& w, int b) { return w.lo[b]; }
+template <class W>
+constexpr bool has_window() { return !std::is_empty<W>::value; }
+
+// Both halves of x where the same half of the probability pair p is not zero:
+// a hidden token's probability is 0, and 0 times what its scale or value may
+// hold (infinities, NaN) must not reach the sums.
+__device__ __forceinline__ uint32_t keep_seen(uint32_t x, uint32_t p) { return x & __vcmpne2(p & 0x7fff7fffu, 0u); }
+
+// Exact-token chunk r of a unit (the items after its quantized blocks; r counts
+// from the window's first ring chunk): ring chunk r while r < ceil(nres / kResChunk), then the sink chunk if the
 // sequence has sinks; an empty sequence's one item is a ring chunk with no
 // tokens. Returns the tokens present (<= 0 for none) and whether it is the
 // sink chunk.
-__device__ __forceinline__ int exact_chunk(const DecodeParams& p, int b, int r, bool& sink) {
+template <class W>
+__device__ __forceinline__ int exact_chunk(const DecodeParams& p, const W& win, int b, int r, bool& sink) {
   const int nres = p.nres[b];
+  r += first_chunk(win, b);
   sink = false;
   if (r < (nres + kResChunk - 1) / kResChunk) return nres - r * kResChunk;
   const int nsink = p.L.sinks > 0 ? p.L.lens[(int64_t)b * kLensStride + kLenS] : 0;
@@ -725,22 +750,23 @@ __device__ __forceinline__ int exact_chunk(const DecodeParams& p, int b, int r, 
 // also stores it into its ring slot for later calls (no other item of this
 // call reads that slot), and the unit of KV head 0 records the sequence's new
 // lengths.
-__device__ __forceinline__ void store_new_token(const DecodeParams& p, int b, int h, int nb, const uint8_t* stage,
+// nq: the sequence's quantized tokens.
+__device__ __forceinline__ void store_new_token(const DecodeParams& p, int b, int h, int nq, const uint8_t* stage,
                                                 int lane) {
   const LayerView& L = p.L;
   const int i = p.nres[b] - 1;
   const int row = i % kResChunk;
-  const int slot = (nb * L.tile_tokens + i) % L.residual;
+  const int slot = (nq + i) % L.residual;
   const int64_t dst = (((int64_t)b * L.num_kv_heads + h) * L.residual + slot) * kRowBytes;
   reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(L.ring_k) + dst)[lane] =
       reinterpret_cast<const uint2*>(stage + row * kRowBytes)[lane];
   reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(L.ring_v) + dst)[lane] =
       reinterpret_cast<const uint2*>(stage + (kResChunk + row) * kRowBytes)[lane];
-  if (h == 0 && lane == 0) {  // the step's lengths (a flush of this step moved G tokens to block nb - 1)
+  if (h == 0 && lane == 0) {  // the step's lengths (a flush of this step moved G tokens to the last block)
     int32_t* len = L.lens + (int64_t)b * kLensStride;
-    len[kLenQ] = nb * L.tile_tokens;
+    len[kLenQ] = nq;
     len[kLenN] = p.nres[b];
-    len[kLenQV] = nb * L.tile_tokens;
+    len[kLenQV] = nq;
   }
 }
 
@@ -759,8 +785,9 @@ struct IssueState {
 // Issues the copy of work item k (a block record, or the key and value rows
 // of a ring chunk) into stage `dst`, completing on `bar`; on the first item
 // of a unit also the unit's queries, into the next query buffer (qslot).
-__device__ __forceinline__ void issue_item(const DecodeParams& p, const MmaPlan& mp, IssueState& is, int k,
-                                           uint8_t* dst, uint64_t* bar, uint8_t* qbuf, int NG) {
+template <class W>
+__device__ __forceinline__ void issue_item(const DecodeParams& p, const MmaPlan& mp, const W& win, IssueState& is,
+                                           int k, uint8_t* dst, uint64_t* bar, uint8_t* qbuf, int NG) {
   const LayerView& L = p.L;
   UnitCursor& u = is.u;
   u.advance(p, k);
@@ -771,11 +798,12 @@ __device__ __forceinline__ void issue_item(const DecodeParams& p, const MmaPlan&
   if (newq) {
     is.unit = unit;
     is.qslot = is.qslot + 1 == mp.nstages ? 0 : is.qslot + 1;
-    is.ring0 = (nb * L.tile_tokens) % L.residual;
+    is.ring0 = ((first_tile(win, u.b) + nb) * L.tile_tokens) % L.residual;
   }
   if (j < nb) {
     // tile item j: tile j % NT of block j / NT (NT = 2^lg_nt tiles per block)
-    const int jb = j >> mp.lg_nt, jt = j & ((1 << mp.lg_nt) - 1);
+    const int jw = first_tile(win, u.b) + j;
+    const int jb = jw >> mp.lg_nt, jt = jw & ((1 << mp.lg_nt) - 1);
     mbar_expect_tx(bar, mp.tx_bytes + (newq ? qbytes : 0u));
     const uint8_t* rec;
     if (L.page_table) {  // one page-table read per run of page_blocks blocks of the unit
@@ -811,14 +839,15 @@ __device__ __forceinline__ void issue_item(const DecodeParams& p, const MmaPlan&
     // ring chunk: kResChunk consecutive slots of keys, then of values (or
     // the kResChunk sink rows of the unit)
     bool sink;
-    (void)exact_chunk(p, u.b, j - nb, sink);
+    (void)exact_chunk(p, win, u.b, j - nb, sink);
+    const int rc = first_chunk(win, u.b) + j - nb;  // ring chunk
     const void* ksrc = sink ? L.sink_k : L.ring_k;
     const void* vsrc = sink ? L.sink_v : L.ring_v;
     int64_t row;
     if (sink) {
       row = ((int64_t)u.b * L.num_kv_heads + u.h) * KVQ_MAX_SINKS;
     } else {
-      int slot = is.ring0 + (j - nb) * kResChunk;  // (j - nb) * kResChunk < residual
+      int slot = is.ring0 + rc * kResChunk;  // rc * kResChunk < residual
       if (slot >= L.residual) slot -= L.residual;
       row = ((int64_t)u.b * L.num_kv_heads + u.h) * L.residual + slot;
     }
@@ -826,7 +855,7 @@ __device__ __forceinline__ void issue_item(const DecodeParams& p, const MmaPlan&
     mbar_expect_tx(bar, 2 * bytes + (newq ? qbytes : 0u));
     const uint8_t* kr = reinterpret_cast<const uint8_t*>(ksrc) + row * kRowBytes;
     const uint8_t* vr = reinterpret_cast<const uint8_t*>(vsrc) + row * kRowBytes;
-    if (p.new_k && !sink && j - nb == (p.nres[u.b] - 1) / kResChunk) {
+    if (p.new_k && !sink && rc == (p.nres[u.b] - 1) / kResChunk) {
       // fused decode step: row i of this chunk is the new token, from the
       // input; the ring rows around it as they are
       const int i = (p.nres[u.b] - 1) % kResChunk;
@@ -861,9 +890,11 @@ __device__ __forceinline__ void issue_item(const DecodeParams& p, const MmaPlan&
 
 // PT: keys per token over whole head vectors, with the rotation when the
 // layer has it (see unit_query); otherwise per-channel keys.
-template <int KB, int VB, int NGRP, int NKT, bool PT>
-__global__ void __launch_bounds__(kThreads, 2) decode_tc_kernel(DecodeParams p, MmaPlan mp) {
+// W: NoWindow, or the tables of a sliding window.
+template <int KB, int VB, int NGRP, int NKT, bool PT, class W>
+__global__ void __launch_bounds__(kThreads, 2) decode_tc_kernel(DecodeParams p, MmaPlan mp, W win) {
   using S = Shape<KB, VB, NGRP, NKT>;
+  constexpr bool WIN = has_window<W>();
   constexpr int D = S::D;
   extern __shared__ __align__(128) uint8_t smem[];
   const int c = blockIdx.x;
@@ -899,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_tc_kernel(DecodeParams p, 
     for (int i = 0; i < SPW; ++i) mbar_init(full + i, 1);
     fence_mbar_init();
     for (int n = 0; n < SPW && n < nmine; ++n)
-      issue_item(p, mp, is, rs + warp + n * kNC, stages + (size_t)n * mp.stage_bytes, full + n, qbuf, NG);
+      issue_item(p, mp, win, is, rs + warp + n * kNC, stages + (size_t)n * mp.stage_bytes, full + n, qbuf, NG);
   }
   __syncwarp();
   bool failed = false;
@@ -989,6 +1020,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_tc_kernel(DecodeParams p, 
         const int j = kb - u.start;
         if (j < nb) {
           // ============ quantized block
+          // positions of the tile below the window (the first tile only)
+          const int skip = WIN && j == 0 ? first_seen(win, u.b) - first_tile(win, u.b) * G : 0;
           if constexpr (PT) {
             if (!uq_ready) {
               unit_query<NKT>(qw, ws, mp, NG, lane, p.score_scale, L.hadamard != 0);
@@ -1062,6 +1095,19 @@ __global__ void __launch_bounds__(kThreads, 2) decode_tc_kernel(DecodeParams p, 
                     sc[mt][r * HPL + h] = fmaf(head_score<NKT>(Dk[mt], r, h), rs, bias[h]);
                 }
               }
+            if constexpr (WIN) {
+              if (skip > 0) {
+#pragma unroll
+                for (int mt = 0; mt < S::MT; ++mt)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r)
+                    if (tile_token<KB>(mt, g + 8 * r) < skip) {
+#pragma unroll
+                      for (int h = 0; h < HPL; ++h) sc[mt][r * HPL + h] = -INFINITY;
+                    }
+              }
+            }
+            // (the tile's last token is seen, so that every head keeps a finite score)
             softmax_update<S::MT, HPL, NGRP, false>(sc, sst, valid, O, Z, lane);
             // ---- values: O += codes x (p * s), Z += ones x (p * z)
 #pragma unroll
@@ -1079,7 +1125,15 @@ __global__ void __launch_bounds__(kThreads, 2) decode_tc_kernel(DecodeParams p, 
               uint32_t R0[PT ? NGRP : 1], R1[PT ? NGRP : 1];
 #pragma unroll
               for (int gg = 0; gg < NGRP; ++gg) {
-                const uint4 v4 = vsz4[(kst * 4 + t) * NGRP + gg];  // (s, s), (s, s), (z, z), (z, z) of rows 2t.. 9+2t
+                uint4 v4 = vsz4[(kst * 4 + t) * NGRP + gg];  // (s, s), (s, s), (z, z), (z, z) of rows 2t.. 9+2t
+                if constexpr (WIN) {
+                  if (skip > 0) {
+                    v4.x = keep_seen(v4.x, bt);
+                    v4.y = keep_seen(v4.y, bb);
+                    v4.z = keep_seen(v4.z, bt);
+                    v4.w = keep_seen(v4.w, bb);
+                  }
+                }
                 B0[gg] = hmul2(bt, v4.x);
                 B1[gg] = hmul2(bb, v4.y);
                 // PT: whole-vector value groups have scales and zero points
@@ -1135,24 +1189,29 @@ __global__ void __launch_bounds__(kThreads, 2) decode_tc_kernel(DecodeParams p, 
             uq_ready = false;  // ring_chunk writes its own query over the B fragments
           }
           bool sink;
-          const int cnt0 = exact_chunk(p, u.b, j - nb, sink);
+          const int cnt0 = exact_chunk(p, win, u.b, j - nb, sink);
+          const int rc = first_chunk(win, u.b) + j - nb;  // ring chunk
+          const int nq = (first_tile(win, u.b) + nb) * G;  // quantized tokens
+          const int skip = WIN && !sink ? first_seen(win, u.b) - nq - rc * kResChunk : 0;
           // tokens of the chunk each lane head sees: a ring chunk hides its
           // last lag_base - t tokens from query token t (several per sequence)
           int cnt[HPL];
 #pragma unroll
           for (int h = 0; h < HPL; ++h)
             cnt[h] = sink ? cnt0 : cnt0 - (p.lag_base - (HPL == 2 ? 2 * t + h : t) / ngr);
-          if (p.new_k && !sink && j - nb == (p.nres[u.b] - 1) / kResChunk) store_new_token(p, u.b, u.h, nb, stage, lane);
+          if (p.new_k && !sink && rc == (p.nres[u.b] - 1) / kResChunk) store_new_token(p, u.b, u.h, nq, stage, lane);
           if (bf16)
-            ring_chunk<true, VB, NGRP, NKT>(stage, qw, bkw, cnt, NG, lane, p.score_scale, valid, rq_ready, sst, O, Z);
+            ring_chunk<true, VB, NGRP, NKT, WIN>(stage, qw, bkw, cnt, skip, NG, lane, p.score_scale, valid, rq_ready,
+                                                 sst, O, Z);
           else
-            ring_chunk<false, VB, NGRP, NKT>(stage, qw, bkw, cnt, NG, lane, p.score_scale, valid, rq_ready, sst, O, Z);
+            ring_chunk<false, VB, NGRP, NKT, WIN>(stage, qw, bkw, cnt, skip, NG, lane, p.score_scale, valid, rq_ready,
+                                                  sst, O, Z);
         }
         // every lane is done with the stage: refill it with item n + SPW
         __syncwarp();
         if (lane == 0 && n + SPW < nmine) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          issue_item(p, mp, is, rs + warp + (n + SPW) * kNC, stages + (size_t)st * mp.stage_bytes, full + st, qbuf, NG);
+          issue_item(p, mp, win, is, rs + warp + (n + SPW) * kNC, stages + (size_t)st * mp.stage_bytes, full + st, qbuf, NG);
         }
         if (++st == SPW) {
           st = 0;
@@ -1217,7 +1276,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_tc_kernel(DecodeParams p, 
 // programmatic dependent of that kernel: its CTAs may start while the flush
 // runs and wait for it (griddepcontrol.wait) before reading any record.
 template <int KB, int VB, int NGRP, int NKT, bool PT>
-cudaError_t launch_instance(const DecodeParams& p, const MmaPlan& mp, cudaStream_t stream) {
+cudaError_t launch_instance(const DecodeParams& p, const MmaPlan& mp, const WindowTables* win, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.num_ctas);
   cfg.blockDim = dim3(kThreads);
@@ -1228,12 +1287,14 @@ cudaError_t launch_instance(const DecodeParams& p, const MmaPlan& mp, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = p.after_flush ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_tc_kernel<KB, VB, NGRP, NKT, PT>, p, mp);
+  if (win) return cudaLaunchKernelEx(&cfg, decode_tc_kernel<KB, VB, NGRP, NKT, PT, WindowTables>, p, mp, *win);
+  return cudaLaunchKernelEx(&cfg, decode_tc_kernel<KB, VB, NGRP, NKT, PT, NoWindow>, p, mp, NoWindow{});
 }
 
 template <int KB, int VB, int NGRP, int NKT, bool PT>
-const void* instance_fn() {
-  return reinterpret_cast<const void*>(decode_tc_kernel<KB, VB, NGRP, NKT, PT>);
+const void* instance_fn(bool win) {
+  return win ? reinterpret_cast<const void*>(decode_tc_kernel<KB, VB, NGRP, NKT, PT, WindowTables>)
+             : reinterpret_cast<const void*>(decode_tc_kernel<KB, VB, NGRP, NKT, PT, NoWindow>);
 }
 
 }  // namespace tc

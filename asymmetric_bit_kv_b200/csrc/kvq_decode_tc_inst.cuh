@@ -17,25 +17,26 @@ namespace tc {
 #define KVQ_TC_VB_NG(X) X(2, 1) X(2, 2) X(4, 1) X(4, 2) X(4, 4) X(8, 1) X(8, 2) X(8, 4)
 #define KVQ_TC_VB_PT(X) X(2, 1) X(4, 1) X(8, 1)
 
-cudaError_t KVQ_TC_LAUNCH(int vb, int ngrp, bool pt, const DecodeParams& p, const MmaPlan& mp, cudaStream_t stream) {
+cudaError_t KVQ_TC_LAUNCH(int vb, int ngrp, bool pt, const DecodeParams& p, const MmaPlan& mp, const WindowTables* win,
+                          cudaStream_t stream) {
 #define KVQ_TC_CASE(V, N) \
-  if (!pt && vb == V && ngrp == N) return launch_instance<KVQ_TC_KB, V, N, KVQ_TC_NKT, false>(p, mp, stream);
+  if (!pt && vb == V && ngrp == N) return launch_instance<KVQ_TC_KB, V, N, KVQ_TC_NKT, false>(p, mp, win, stream);
   KVQ_TC_VB_NG(KVQ_TC_CASE)
 #undef KVQ_TC_CASE
 #define KVQ_TC_CASE(V, N) \
-  if (pt && vb == V && ngrp == N) return launch_instance<KVQ_TC_KB, V, N, KVQ_TC_NKT, true>(p, mp, stream);
+  if (pt && vb == V && ngrp == N) return launch_instance<KVQ_TC_KB, V, N, KVQ_TC_NKT, true>(p, mp, win, stream);
   KVQ_TC_VB_PT(KVQ_TC_CASE)
 #undef KVQ_TC_CASE
   return cudaErrorInvalidValue;
 }
 
-const void* KVQ_TC_FN(int vb, int ngrp, bool pt) {
+const void* KVQ_TC_FN(int vb, int ngrp, bool pt, bool win) {
 #define KVQ_TC_CASE(V, N) \
-  if (!pt && vb == V && ngrp == N) return instance_fn<KVQ_TC_KB, V, N, KVQ_TC_NKT, false>();
+  if (!pt && vb == V && ngrp == N) return instance_fn<KVQ_TC_KB, V, N, KVQ_TC_NKT, false>(win);
   KVQ_TC_VB_NG(KVQ_TC_CASE)
 #undef KVQ_TC_CASE
 #define KVQ_TC_CASE(V, N) \
-  if (pt && vb == V && ngrp == N) return instance_fn<KVQ_TC_KB, V, N, KVQ_TC_NKT, true>();
+  if (pt && vb == V && ngrp == N) return instance_fn<KVQ_TC_KB, V, N, KVQ_TC_NKT, true>(win);
   KVQ_TC_VB_PT(KVQ_TC_CASE)
 #undef KVQ_TC_CASE
   return nullptr;

@@ -8,6 +8,7 @@ is missing this module raises on import of the library: there is no fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -105,6 +106,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kvq_decode_attention": (I32, [P, I32, P, P, I32, F32, I32, P]),
         "kvq_decode_attention_noalloc": (I32, [P, I32, P, P, I32, F32, I32, P]),
         "kvq_decode_step": (I32, [P, I32, P, P, P, P, I32, F32, I32, P]),
+        "kvq_chunk_attention": (I32, [P, I32, P, P, P, P, I32, F32, ctypes.POINTER(I32), I32, I32, P]),
+        "kvq_decode_attention_window": (I32, [P, I32, P, P, I32, F32, I32, I32, P]),
+        "kvq_decode_step_window": (I32, [P, I32, P, P, P, P, I32, F32, I32, I32, P]),
+        "kvq_fork_sequence": (I32, [P, I32, ctypes.POINTER(I32), I32, P]),
         "kvq_dequant": (I32, [P, I32, I32, I32, I32, P, P, P]),
         "kvq_get_layout": (I32, [P, I32, ctypes.POINTER(kvq_layout)]),
         "kvq_device_errors": (I32, [P, ctypes.POINTER(I32)]),
@@ -147,6 +152,11 @@ def _need(t: torch.Tensor, dtype, name):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _need_shape(t: torch.Tensor, shape: tuple, name):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
 
 
 @dataclass
@@ -300,6 +310,96 @@ class KVCache:
                                                      _DTYPE_CODE[out.dtype], float(softmax_scale), q.shape[0],
                                                      _stream_ptr(stream)),
                "kvq_decode_attention_noalloc")
+        return out
+
+    def chunk_attention(self, layer: int, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor, new_lens,
+                        out: torch.Tensor | None = None, out_dtype=torch.float32, softmax_scale: float | None = None,
+                        window: int = 0, stream=None):
+        """A chunk of new tokens per sequence over the cached tokens and,
+        causally, over the chunk itself (kvq_chunk_attention); the cache is only
+        read, so append the same k, v afterwards. k, v: [sum(new_lens), Hkv, D],
+        q: [sum(new_lens), Hq, D] in the cache dtype; new_lens as in append.
+        window: 0, or the tokens a query sees besides the sinks. Returns out
+        [sum(new_lens), Hq, D]."""
+        _need(k, self.cfg.kv_dtype, "k")
+        _need(v, self.cfg.kv_dtype, "v")
+        _need(q, self.cfg.kv_dtype, "q")
+        arr = new_lens if isinstance(new_lens, ctypes.Array) else lens_array(new_lens)
+        cfg, total = self.cfg, sum(arr)
+        _need_shape(k, (total, cfg.num_kv_heads, cfg.head_dim), "k")
+        _need_shape(v, (total, cfg.num_kv_heads, cfg.head_dim), "v")
+        _need_shape(q, (total, cfg.num_q_heads, cfg.head_dim), "q")
+        out = self._out_like(q, out, out_dtype)
+        if softmax_scale is None:
+            softmax_scale = cfg.head_dim ** -0.5
+        with self._on_device(k, v, q, out):
+            _check(self.lib.kvq_chunk_attention(self.handle, layer, k.data_ptr(), v.data_ptr(), q.data_ptr(), out.data_ptr(),
+                                                _DTYPE_CODE[out.dtype], float(softmax_scale), arr, len(arr), window,
+                                                _stream_ptr(stream)),
+                   "kvq_chunk_attention")
+        return out
+
+    def decode_attention_window(self, layer: int, q: torch.Tensor, window: int, out: torch.Tensor | None = None,
+                                out_dtype=torch.float32, softmax_scale: float | None = None, stream=None):
+        """decode_attention over the last `window` tokens and the sinks of every
+        sequence (kvq_decode_attention_window). q: [batch, Hq, D]."""
+        _need(q, self.cfg.kv_dtype, "q")
+        _need_shape(q, (q.shape[0], self.cfg.num_q_heads, self.cfg.head_dim), "q")
+        out = self._out_like(q, out, out_dtype)
+        if softmax_scale is None:
+            softmax_scale = self.cfg.head_dim ** -0.5
+        with self._on_device(q, out):
+            _check(self.lib.kvq_decode_attention_window(self.handle, layer, q.data_ptr(), out.data_ptr(),
+                                                        _DTYPE_CODE[out.dtype], float(softmax_scale), q.shape[0], window,
+                                                        _stream_ptr(stream)),
+                   "kvq_decode_attention_window")
+        return out
+
+    def decode_step_window(self, layer: int, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor, window: int,
+                           out: torch.Tensor | None = None, out_dtype=torch.float32,
+                           softmax_scale: float | None = None, stream=None):
+        """decode_step over the last `window` tokens and the sinks
+        (kvq_decode_step_window). k, v: [batch, Hkv, D], q: [batch, Hq, D]."""
+        cfg = self.cfg
+        for t, h, name in ((k, cfg.num_kv_heads, "k"), (v, cfg.num_kv_heads, "v"), (q, cfg.num_q_heads, "q")):
+            _need(t, cfg.kv_dtype, name)
+            _need_shape(t, (q.shape[0], h, cfg.head_dim), name)
+        out = self._out_like(q, out, out_dtype)
+        if softmax_scale is None:
+            softmax_scale = cfg.head_dim ** -0.5
+        with self._on_device(k, v, q, out):
+            _check(self.lib.kvq_decode_step_window(self.handle, layer, k.data_ptr(), v.data_ptr(), q.data_ptr(),
+                                                   out.data_ptr(), _DTYPE_CODE[out.dtype], float(softmax_scale), q.shape[0],
+                                                   window, _stream_ptr(stream)),
+                   "kvq_decode_step_window")
+        return out
+
+    def fork_sequence(self, src: int, dsts, stream=None):
+        """Make every sequence of dsts a copy of sequence src in all layers; a
+        paged cache shares the filled pages (kvq_fork_sequence)."""
+        arr = lens_array(dsts)
+        with self._on_device():
+            _check(self.lib.kvq_fork_sequence(self.handle, src, arr, len(arr), _stream_ptr(stream)), "kvq_fork_sequence")
+
+    def _on_device(self, *tensors):
+        """Context in which the cache's device is current; the tensors must be there."""
+        dev = self.arena.device
+        for t in tensors:
+            if t.device != dev:
+                raise ValueError(f"the tensors must be on the cache's device {dev}, got {t.device}")
+        return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    @staticmethod
+    def _out_like(q: torch.Tensor, out: torch.Tensor | None, out_dtype) -> torch.Tensor:
+        """out checked against q, or a new tensor of q's shape."""
+        if out is None:
+            if out_dtype not in _DTYPE_CODE:
+                raise ValueError(f"out_dtype {out_dtype} is not supported")
+            return torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        if out.dtype not in _DTYPE_CODE:
+            raise ValueError(f"out dtype {out.dtype} is not supported")
+        _need(out, out.dtype, "out")
+        _need_shape(out, tuple(q.shape), "out")
         return out
 
     def dequant(self, layer: int, seq: int, t0: int, t1: int, stream=None):

@@ -216,7 +216,8 @@ KVQ_API kvq_status kvq_cache_destroy(kvq_cache* cache);
 KVQ_API kvq_status kvq_cache_reset(kvq_cache* cache, void* stream);
 
 /* Empty sequence `seq` in every layer (stream-ordered) and, in a paged
- * cache, return its pages to the pools. Calls that use the pages again are
+ * cache, return its pages to the pools (a page shared by kvq_fork_sequence
+ * returns with the last sequence that holds it). Calls that use the pages again are
  * ordered after this one on the same stream.                              */
 KVQ_API kvq_status kvq_release_sequence(kvq_cache* cache, int32_t seq, void* stream);
 
@@ -235,7 +236,7 @@ KVQ_API kvq_status kvq_release_sequence(kvq_cache* cache, int32_t seq, void* str
  * max_tokens (sinks included) or, in a paged cache, if the layer's pool has
  * fewer free pages than the call's new blocks need; nothing is enqueued
  * then. A paged cache takes the pages in this call (and in
- * kvq_flush_residual and kvq_decode_step).                                 */
+ * kvq_flush_residual, kvq_decode_step and kvq_fork_sequence).                                 */
 KVQ_API kvq_status kvq_append(kvq_cache* cache, int32_t layer, const void* k, const void* v,
                       const int32_t* new_lens, int32_t batch, void* stream);
 
@@ -330,6 +331,68 @@ KVQ_API kvq_status kvq_decode_attention_noalloc(kvq_cache* cache, int32_t layer,
  * anything is enqueued.                                                   */
 KVQ_API kvq_status kvq_decode_step(kvq_cache* cache, int32_t layer, const void* k, const void* v, const void* q,
                                    void* out, int32_t out_dtype, float softmax_scale, int32_t batch, void* stream);
+
+/* Attention of a chunk of new tokens over the cache (a prompt arriving in
+ * chunks, a follow-up turn, a few drafted tokens): new_lens[b] >= 0 new tokens
+ * of sequence b, whose exact keys and values are k and v, with their queries
+ * q. New token t of a sequence that holds L tokens is its token L + t; its
+ * query attends to the L cached tokens (exact sinks, dequantized blocks, exact
+ * ring tokens) and to the new tokens 0 .. t:
+ *   out[t][h] = softmax_j(scale * q[t][h] . K~_j) V~_j.
+ * The cache is only read: kvq_append the same k, v afterwards (the KIVI
+ * README's prefill, "Overview", attends in full precision and quantizes what
+ * leaves the window; the pages do not describe a prompt in several chunks).
+ * - k, v: device [sum(new_lens)][num_kv_heads][head_dim]; q: device
+ *   [sum(new_lens)][num_q_heads][head_dim], kv_dtype, sequences in order;
+ *   out: device, the shape of q, in out_dtype. All 16-byte aligned.
+ * - window: 0 for none; W >= 1: a query sees the last W tokens up to and
+ *   including its own, and the sequence's first sink_tokens tokens.
+ * - new_lens: host [batch]. A sequence without new tokens is skipped. out is
+ *   written for exactly the new tokens.
+ * - Lengths: L + new_lens[b] may pass max_tokens (the append will then fail),
+ *   but not 2^30.
+ * - Workspace: the arena's split partials, as kvq_decode_attention.
+ * The tensor-core kernel rounds dequantized keys and values to fp16 (once,
+ * from q*d + m) and probabilities to the type of the values they multiply;
+ * scores, softmax statistics and outputs are accumulated in fp32. A
+ * non-finite key or value makes every query row that shares its 128-token
+ * tile undefined, whether the row sees it or not.                          */
+KVQ_API kvq_status kvq_chunk_attention(kvq_cache* cache, int32_t layer, const void* k, const void* v, const void* q,
+                                       void* out, int32_t out_dtype, float softmax_scale, const int32_t* new_lens,
+                                       int32_t batch, int32_t window, void* stream);
+
+/* kvq_decode_attention inside a sliding window: the query (the sequence's
+ * newest token) sees the last `window` tokens (window >= 1) and the sequence's
+ * sink tokens (KV1 card: attention sinks), which stay visible whatever the
+ * window. Blocks outside the window are not read; inside a block that the
+ * window cuts, the hidden tokens' codes are read and their scores dropped, so
+ * what they hold does not matter. A window of at least the sequence's length
+ * gives kvq_decode_attention.                                              */
+KVQ_API kvq_status kvq_decode_attention_window(kvq_cache* cache, int32_t layer, const void* q, void* out,
+                                               int32_t out_dtype, float softmax_scale, int32_t batch, int32_t window,
+                                               void* stream);
+
+/* kvq_decode_step inside a sliding window: one token appended to every
+ * sequence, then kvq_decode_attention_window for q, the new token being the
+ * newest of the window's tokens. Same checks and fusion as kvq_decode_step. */
+KVQ_API kvq_status kvq_decode_step_window(kvq_cache* cache, int32_t layer, const void* k, const void* v,
+                                          const void* q, void* out, int32_t out_dtype, float softmax_scale,
+                                          int32_t batch, int32_t window, void* stream);
+
+/* Make each of the sequences dsts[0 .. num_dsts) a copy of sequence src in
+ * every layer (several samples or beams of one prompt), stream-ordered; what
+ * a destination held before is released. dsts: host, distinct, none equal to
+ * src. Afterwards the sequences are independent: appending to one does not
+ * change another.
+ * - Contiguous cache: block records, rings, sinks and lengths are copied.
+ * - Paged cache: the pages that src has filled are shared (each page counts
+ *   the sequences that hold it and returns to the pool with the last one);
+ *   the partly filled last page, the rings, the sinks and the lengths are
+ *   copied. Fails with KVQ_ERR_CAPACITY, changing nothing, if some layer's
+ *   pool cannot give every destination its page.
+ * No counterpart on the pages: the cache side of parallel sampling.         */
+KVQ_API kvq_status kvq_fork_sequence(kvq_cache* cache, int32_t src, const int32_t* dsts, int32_t num_dsts,
+                                     void* stream);
 
 /* Reconstruct tokens [t0, t1) of sequence `seq` as fp32: x_hat = q*d + m
  * (an fp32 product, then an fp32 sum; KV1 card, BQ2_0) for quantized tokens
