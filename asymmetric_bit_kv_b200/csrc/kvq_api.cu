@@ -458,6 +458,59 @@ kvq_status check_window(const kvq_cache* c, int32_t window) {
   return check_device(c);
 }
 
+// Work items of the tensor-core chunk kernel: a unit is (sequence, KV head,
+// 256 query rows); where there are fewer units than SMs, the tokens of a unit
+// are cut into ranges so that every SM gets about the same number of tile
+// steps, as far as the arena's partial slots hold the parts.
+kvq_status plan_chunk(const kvq_cache* c, kvq::ChunkParams& p) {
+  const kvq_config& cfg = c->cfg;
+  const int ngr = cfg.num_q_heads / cfg.num_kv_heads, hkv = cfg.num_kv_heads;
+  const int64_t sms = std::max(1, c->sm_count), room = (int64_t)cfg.max_batch * cfg.num_q_heads * c->slots;
+  thread_local std::vector<int64_t> tiles, units;  // per entry: tiles of its last unit, units
+  tiles.resize(p.nseq);
+  units.resize(p.nseq);
+  int64_t all = 0, steps = 0;
+  for (int x = 0; x < p.nseq; ++x) {
+    const int64_t rows = (int64_t)p.t_new[x] * ngr;
+    units[x] = hkv * ((rows + 2 * kvq::kChunkSlotRows - 1) / (2 * kvq::kChunkSlotRows));
+    const int64_t seen = p.window > 0 ? (int64_t)p.window + 2 * kvq::kChunkSlotRows / ngr : INT64_MAX;
+    const int64_t exact = std::min<int64_t>(seen, p.s[x] + p.n_len[x] + p.t_new[x]);
+    const int64_t quant = std::min<int64_t>(p.q_len[x], std::max<int64_t>(0, seen - p.n_len[x]));
+    tiles[x] = (quant + kvq::kChunkTile - 1) / kvq::kChunkTile + (exact + kvq::kChunkTile - 1) / kvq::kChunkTile;
+    all += units[x];
+    steps += units[x] * tiles[x];
+  }
+  // tiles per range: one range per SM, but at least 4 tiles (a range's start
+  // and its merge cost about as much)
+  int64_t target = all >= sms ? INT64_MAX : std::max<int64_t>(4, (steps + sms - 1) / sms);
+  for (bool alternate = true;; target = target > (INT64_MAX >> 2) ? INT64_MAX : target * 2) {
+    int64_t items = 0, records = 0, merged = 0;
+    bool fits = true;
+    for (int x = 0; x < p.nseq && fits; ++x) {
+      const int64_t rows = (int64_t)p.t_new[x] * ngr;
+      const int64_t ns = target == INT64_MAX ? 1 : std::min<int64_t>(64, (tiles[x] + target - 1) / target);
+      p.splits[x] = (int32_t)(alternate && rows <= kvq::kChunkSlotRows && tiles[x] > 1 ? -ns : ns);
+      const int parts = kvq::chunk_parts(p.splits[x]);
+      p.item0[x] = (int32_t)items;
+      p.merge0[x] = (int32_t)merged;
+      p.part0[x] = (int32_t)records;
+      items += units[x] * ns;
+      if (parts > 1) {
+        merged += rows * hkv;
+        records += rows * hkv * parts;
+      }
+      if (items > INT32_MAX) return fail(KVQ_ERR_UNSUPPORTED, "too many query rows in one call");
+      fits = records <= room && records <= INT32_MAX;
+    }
+    if (fits) {
+      p.items = (int32_t)items;
+      p.merge_rows = (int32_t)merged;
+      return KVQ_OK;
+    }
+    if (target == INT64_MAX) alternate = false;  // one part a row: always fits
+  }
+}
+
 // kvq_fork_sequence after its argument checks.
 kvq_status enqueue_fork(kvq_cache* c, int src, const int32_t* dsts, int nd, cudaStream_t stream) {
   const kvq_config& cfg = c->cfg;
@@ -1125,16 +1178,27 @@ kvq_status kvq_chunk_attention(kvq_cache* c, int32_t layer, const void* k, const
     off += new_lens[b];
   }
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int64_t items = 0;
-  const int ngr = cfg.num_q_heads / cfg.num_kv_heads;
-  for (int x = 0; x < p.nseq; ++x) {
-    p.item0[x] = (int32_t)items;
-    items += (int64_t)cfg.num_kv_heads * (((int64_t)p.t_new[x] * ngr + kvq::kChunkRows - 1) / kvq::kChunkRows);
-    if (items > INT32_MAX) return fail(KVQ_ERR_UNSUPPORTED, "too many query rows in one call");
+  cudaError_t e;
+  if (kvq::chunk_tc_supported(p.L)) {
+    p.ws_o = reinterpret_cast<float*>(c->arena + c->ws_o_off);
+    p.ws_ml = reinterpret_cast<float2*>(c->arena + c->ws_ml_off);
+    p.err = reinterpret_cast<int32_t*>(c->arena + c->err_off);
+    s = plan_chunk(c, p);
+    if (s != KVQ_OK) return s;
+    e = kvq::launch_chunk_tc(p, st);
+    if (e == cudaSuccess) c->launches += p.merge_rows > 0 ? 2 : 1;  // the attention kernel, the merge of its parts
+  } else {
+    int64_t items = 0;
+    const int ngr = cfg.num_q_heads / cfg.num_kv_heads;
+    for (int x = 0; x < p.nseq; ++x) {
+      p.item0[x] = (int32_t)items;
+      items += (int64_t)cfg.num_kv_heads * (((int64_t)p.t_new[x] * ngr + kvq::kChunkRows - 1) / kvq::kChunkRows);
+      if (items > INT32_MAX) return fail(KVQ_ERR_UNSUPPORTED, "too many query rows in one call");
+    }
+    p.items = (int32_t)items;
+    e = kvq::launch_chunk_simple(p, st);
+    if (e == cudaSuccess) ++c->launches;
   }
-  p.items = (int32_t)items;
-  const cudaError_t e = kvq::launch_chunk_simple(p, st);
-  if (e == cudaSuccess) ++c->launches;
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
   return KVQ_OK;
 }

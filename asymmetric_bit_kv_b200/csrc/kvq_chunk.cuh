@@ -32,11 +32,33 @@ struct ChunkParams {
   int32_t t_new[KVQ_MAX_BATCH];   // new tokens
   int32_t in_off[KVQ_MAX_BATCH];  // first row of the sequence in k, v, q and out
   int32_t item0[KVQ_MAX_BATCH];   // first work item
+  // Tensor-core kernel: how a sequence's units (KV head, tile of query rows)
+  // are cut. splits > 0: so many ranges of the tokens, both slots of a CTA on
+  // every tile (256 rows); splits < 0: -splits ranges, the slots on alternate
+  // tiles (at most 128 rows). A row of several parts leaves part j at record
+  // part0 + (h * rows + r) * parts + j of ws_o / ws_ml, and the merge kernel
+  // joins the rows merge0 .. of all entries (entries of one part take none).
+  float* ws_o;          // [records][D]
+  float2* ws_ml;        // [records]: (maximum in log2 units, sum)
+  int32_t* err;
+  int32_t merge_rows;
+  int32_t splits[KVQ_MAX_BATCH];
+  int32_t merge0[KVQ_MAX_BATCH];
+  int32_t part0[KVQ_MAX_BATCH];
 };
+// Parts of each row of an entry with these splits.
+__host__ __device__ inline int chunk_parts(int splits) { return splits < 0 ? -2 * splits : splits; }
 
 constexpr int kChunkRows = 16;  // query rows (token, head) of one CTA of the CUDA-core kernel
 
 // The CUDA-core kernel: every cache format.
 cudaError_t launch_chunk_simple(const ChunkParams& p, cudaStream_t stream);
+
+// The tensor-core kernel and the merge of its parts: layers whose keys and
+// values share one residual length.
+constexpr int kChunkSlotRows = 128;  // query rows of one slot; a CTA has two
+constexpr int kChunkTile = 128;      // tokens of a tile
+bool chunk_tc_supported(const LayerView& L);
+cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream);
 
 }  // namespace kvq

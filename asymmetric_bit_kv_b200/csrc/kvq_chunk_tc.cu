@@ -1,0 +1,1071 @@
+// Chunk attention on the tensor cores (tcgen05, tensor memory): layers whose
+// keys and values share one residual length.
+//
+// Method: the formula of kvq_chunk.cu. A work item is one (sequence, KV head,
+// tile of query rows); a row is (new token, query head of the KV head), so all
+// query heads of a KV head share every dequantized key and value. The item
+// walks the tokens its rows see in tiles of 128: first the quantized positions
+// (phase A, tiles of positions 128a ..), then the exact tokens (phase B: the
+// list sinks, ring, new tokens, in order). Per tile: S = Q K^T (128x128x128
+// per slot), online softmax, O += P V.
+//
+// Why this shape. Two slots of 128 rows use all 512 columns of tensor memory
+// (S0 | S1 | O0 | O1, fp32; P overwrites S as 16-bit pairs) and alternate: one
+// slot's softmax runs while the tensor cores work on the other's products.
+//  * More than 128 rows: both slots walk the same tiles (256 rows share each
+//    dequantized tile).
+//  * At most 128 rows: the slots take alternate tiles, each a part of its own.
+// An item may also cover only a range of the tiles (few rows, long caches);
+// parts are merged by chunk_combine_kernel.
+//
+// Warps: 0-3 and 4-7 the softmax of slots 0 and 1 (a thread owns a row, so
+// maxima, sums and the rotation of a row need no exchange), 8-9 key tiles,
+// 10-11 value tiles, 12 issues the MMAs. Registers move from the producers to
+// the softmax warps (setmaxnreg: 184 + 184 + 88 + 56 = 4 x 128).
+//
+// Operands. Phase A: codes become fp16 in three instructions per pair (mask
+// into the mantissa of 1024, subtract, one fma q*d + m: the only rounding).
+// Keys are packed along tokens and values along channels, so expanding a row
+// of codes gives both operands with tokens (channels) contiguous: MN-major B
+// tiles with 128-byte swizzle. A word's codes come out in extraction order
+// (i, i + n/2), which permutes the tokens of a key tile: value rows are stored
+// in the same order (their channels are put back by one permute per pair).
+// Queries are scaled by a power of two per row (exact but for
+// subnormals), so that any bf16 query fits fp16. Phase B: keys, values,
+// queries and probabilities in the kv dtype, keys K-major.
+// Softmax: probabilities are 2^(z - m + 8) with m raised only when a row's
+// maximum grows by more than 4 (log2 units): O is rescaled rarely, and fp16
+// probabilities keep 14 + 8 binary orders below the maximum before they turn
+// subnormal.
+//
+// Every wait is bounded (~2 s): a thread that gives up sets the device error
+// word and an abort flag that ends the others' waits.
+#include <algorithm>
+
+#include "kvq_chunk.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int kRows = kChunkSlotRows, kTile = kChunkTile, kD = kHeadDim;
+constexpr int kThreads = 512;
+constexpr int kKStages = 2, kVStages = 3;
+constexpr int kTileBytes = kTile * kD * 2;
+constexpr int kHalf = kTileBytes / 2;  // one 64-wide block of a tile: 128 rows of 128 bytes
+constexpr int kQOff = 0, kKOff = 2 * kTileBytes, kVOff = kKOff + kKStages * kTileBytes;
+constexpr int kBarOff = kVOff + kVStages * kTileBytes;
+constexpr int kSmemBytes = kBarOff + 256 + 1024;  // + alignment of the base to 1024
+constexpr int kTmemS = 0, kTmemO = 256;           // columns of slot 0; slot 1 is 128 further
+constexpr float kLazy = 4.f, kOffset = 8.f;
+constexpr long long kWaitCycles = 4000000000LL;
+
+// ------------------------------------------------------------- PTX helpers
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits for the phase with the given parity; false when the item was aborted
+// (by this thread after ~2 s, or by another one).
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try(bar, parity)) {
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// The same by a whole warp: all lanes go on, or none.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+// 32 columns of this warp's 32 lanes, one lane per thread.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15])::"memory");
+}
+// Orders the loaded registers after the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool present) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(present ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint32_t bits2(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return bits2(__floats2half2_rn(lo, hi));
+  }
+}
+
+// Shared-memory descriptors: start >> 4, leading and stride byte offsets >> 4,
+// version 1 (bit 46), 128-byte swizzle (2 at bit 61). K-major tiles: rows of
+// 64 k-elements (128 bytes), 8-row groups 1024 bytes apart. MN-major tiles:
+// rows of 64 mn-elements, one k each, 8-k groups 1024 bytes apart and the
+// second 64 mn-elements kHalf further.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(kHalf >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: fp32 accumulator, A and B f16 or bf16, B MN-major or
+// K-major, N = M = 128.
+__device__ __forceinline__ uint32_t inst_desc(bool bf16, bool b_mn) {
+  const uint32_t t = bf16 ? 1u : 0u;
+  return (1u << 4) | (t << 7) | (t << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(kTile >> 3) << 17) |
+         ((uint32_t)(kRows >> 4) << 24);
+}
+
+// ------------------------------------------------------------------ the item
+struct Item {
+  int i, b, h;          // table entry, sequence, KV head
+  int ngr, rows, r0;    // query heads per KV head, rows of the unit, first row of the item
+  bool both;            // both slots walk every tile (else alternate tiles)
+  int t0, t1;           // first and last new token of the item's rows
+  int s, q, n;          // sinks, quantized positions, ring tokens
+  int nA, a0;           // phase A: tiles a0 .. a0 + nA - 1 of positions
+  int nB, b0, b_sink;   // phase B: tile 0 first if b_sink, then tiles b0 ..
+  int k0, k1;           // the item's range of the nA + nB tiles
+  int part, parts;      // first part of the item, parts of the unit's rows
+  int first_e;          // phase B entries below this stay visible outside the window
+
+  __device__ __forceinline__ int tile_b(int k) const {  // phase B tile of k >= nA
+    const int j = k - nA;
+    return b_sink ? (j == 0 ? 0 : b0 + j - 1) : b0 + j;
+  }
+  __device__ __forceinline__ int steps() const { return both ? 2 * (k1 - k0) : k1 - k0; }
+  // tiles of slot w, and its j-th one
+  __device__ __forceinline__ int slot_tiles(int w) const { return both ? k1 - k0 : (k1 - k0 + 1 - w) / 2; }
+  __device__ __forceinline__ int slot_tile(int w, int j) const { return both ? k0 + j : k0 + 2 * j + w; }
+};
+
+__device__ __forceinline__ Item find_item(const ChunkParams& p, int idx) {
+  Item it;
+  int lo = 0, hi = p.nseq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.item0[mid] <= idx) lo = mid;
+    else hi = mid - 1;
+  }
+  const int hkv = p.L.num_kv_heads;
+  it.i = lo;
+  it.b = p.seq[lo];
+  it.ngr = p.num_q_heads / hkv;
+  it.rows = p.t_new[lo] * it.ngr;
+  it.both = p.splits[lo] > 0;
+  const int ns = abs(p.splits[lo]), tiles = (it.rows + 2 * kRows - 1) / (2 * kRows);
+  int x = idx - p.item0[lo];
+  const int sp = x % ns;
+  x /= ns;
+  it.h = x % hkv;
+  it.r0 = (tiles - 1 - x / hkv) * 2 * kRows;  // the rows that see most first
+  it.t0 = it.r0 / it.ngr;
+  it.t1 = (min(it.r0 + 2 * kRows, it.rows) - 1) / it.ngr;
+  it.s = p.s[lo];
+  it.q = p.q_len[lo];
+  it.n = p.n_len[lo];
+  const int after = it.n + it.t0 - p.window + 1;  // first visible entry past the quantized positions, if >= 0
+  const int low_a = p.window > 0 ? max(0, it.q + after) : 0;
+  it.a0 = low_a / kTile;
+  it.nA = low_a >= it.q ? 0 : (it.q + kTile - 1) / kTile - it.a0;
+  it.first_e = it.q > 0 ? it.s : p.sink_tokens;
+  const int low_b = p.window > 0 ? max(0, it.s + after) : 0;
+  it.b0 = low_b / kTile;
+  it.b_sink = it.first_e > 0 && it.b0 > 0 ? 1 : 0;
+  it.nB = (it.s + it.n + it.t1 + kTile) / kTile - it.b0 + it.b_sink;
+  const int64_t total = it.nA + it.nB;
+  it.k0 = (int)(total * sp / ns);
+  it.k1 = (int)(total * (sp + 1) / ns);
+  it.parts = chunk_parts(p.splits[lo]);
+  it.part = it.both ? sp : 2 * sp;
+  return it;
+}
+
+// ----------------------------------------------------------------- producers
+// Four fp16 pairs of a 4-bit word's codes (i, i + 4), eight of a 2-bit word's
+// (i, i + 8), two of an 8-bit word's (2i, 2i + 1), as exact integers.
+template <int B>
+__device__ __forceinline__ __half2 code_pair(uint32_t w, uint32_t w8, int i) {
+  if constexpr (B == 8) {
+    return __hsub2(half2_of(__byte_perm(w, 0x64646464u, i == 0 ? 0x4140 : 0x4342)), half2_of(0x64006400u));
+  } else {
+    constexpr int per = 8 / B;  // code positions in a byte
+    const int k = i % per;
+    const uint32_t m = ((1u << B) - 1u) << (B * k);
+    const uint32_t x = ((i < per ? w : w8) & (m | (m << 16))) | 0x64006400u;  // 1024 + code * 2^(B k)
+    if (k == 0) return __hsub2(half2_of(x), half2_of(0x64006400u));
+    const __half f = __float2half_rn(1.f / (float)(1 << (B * k))), o = __float2half_rn(-1024.f / (float)(1 << (B * k)));
+    return __hfma2(half2_of(x), __half2half2(f), __half2half2(o));
+  }
+}
+template <int B>
+constexpr int codes_per_word() { return 32 / B; }
+// Place of code j of a word in extraction order, and the code at place c.
+__host__ __device__ inline int place_of(int j, int per) {
+  return per == 4 ? j : (j < per / 2 ? 2 * j : 2 * (j - per / 2) + 1);
+}
+__host__ __device__ inline int code_at(int c, int per) { return per == 4 ? c : ((c & 1) ? per / 2 : 0) + (c >> 1); }
+
+// Expands 64 codes (2 * B words) into a 128-byte row of fp16 at `row`, chunk
+// c at c ^ x. sz(place) gives the (scale, zero point) half2 pairs of the two
+// codes at places 2i, 2i + 1: {(s, s), (z, z)}.
+// NATURAL: the codes' own order instead, one more permute per pair.
+template <int B, bool NATURAL, class SZ>
+__device__ __forceinline__ void expand_row(const uint32_t (&w)[2 * B], uint32_t row, int x, SZ sz) {
+  constexpr int per = 32 / B, pairs = per / 2;
+#pragma unroll
+  for (int j = 0; j < 2 * B; ++j) {
+    const uint32_t w8 = w[j] >> 8;
+    uint32_t h[pairs];
+#pragma unroll
+    for (int i = 0; i < pairs; ++i) {
+      uint32_t s2, z2;
+      sz(j * pairs + i, s2, z2);
+      h[i] = bits2(__hfma2(code_pair<B>(w[j], w8, i), half2_of(s2), half2_of(z2)));
+    }
+    if constexpr (NATURAL && B != 8) {
+      uint32_t o[pairs];
+#pragma unroll
+      for (int i = 0; i < pairs / 2; ++i) {
+        o[i] = __byte_perm(h[2 * i], h[2 * i + 1], 0x5410);
+        o[pairs / 2 + i] = __byte_perm(h[2 * i], h[2 * i + 1], 0x7632);
+      }
+#pragma unroll
+      for (int i = 0; i < pairs; ++i) h[i] = o[i];
+    }
+    if constexpr (B == 8) {  // two words fill a chunk
+      const uint32_t at = row + (((j >> 1) ^ x) << 4) + 8 * (j & 1);
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(h[0]), "r"(h[1]) : "memory");
+    } else {
+#pragma unroll
+      for (int c = 0; c < pairs / 4; ++c)
+        sts16(row + (((j * (pairs / 4) + c) ^ x) << 4), h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+    }
+  }
+}
+__device__ __forceinline__ void zero_row(uint32_t row) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) sts16(row + (c << 4), 0u, 0u, 0u, 0u);
+}
+
+// 64 key codes of channel d at positions p0 .. p0 + 63 (p0 a multiple of 64),
+// in token order, with the scales of their one or two blocks.
+template <int KB>
+struct KeyRow {
+  uint32_t w[2 * KB];
+  uint32_t sz[2];     // per channel: (scale, zero) of tokens 0-31 and 32-63
+  const uint32_t* tok;  // per token: (scale, zero) pairs of the channel's group, first block
+  const uint32_t* tok2;
+  int valid;          // tokens present: 0, 32 or 64
+};
+template <int KB>
+__device__ __forceinline__ void load_key_row(const LayerView& L, int b, int h, int p0, int q, int d, KeyRow<KB>& r) {
+  r.valid = min(64, max(0, q - p0));
+  if (r.valid == 0) return;
+  const int G = L.group_k;
+  const uint8_t* rec = record_ptr(L, b, h, p0 / G);
+  if (G >= 64) {
+    const uint8_t* tp = rec + L.tile0_off + (G > 64 ? (int64_t)((p0 / 64) & 1) * L.tile_bytes : 0);
+    const uint4* kc = reinterpret_cast<const uint4*>(tp + L.kc_off) + d * (KB / 2);
+    const int x = chunk_swizzle(d, KB / 2);
+#pragma unroll
+    for (int c = 0; c < KB / 2; ++c) {
+      const uint4 v = __ldg(kc + (c ^ x));
+      r.w[4 * c] = v.x, r.w[4 * c + 1] = v.y, r.w[4 * c + 2] = v.z, r.w[4 * c + 3] = v.w;
+    }
+    if (L.k_axis == 0) {
+      const uint8_t* k = L.rec_ksz_off >= 0 ? rec + L.rec_ksz_off : tp + L.ksz_off;
+      r.sz[0] = r.sz[1] = __ldg(reinterpret_cast<const uint32_t*>(k) + d);
+    } else {
+      r.tok = reinterpret_cast<const uint32_t*>(tp + L.ksz_off) + d / L.group_v;
+      r.tok2 = r.tok + 32 * (kD / L.group_v);
+    }
+  } else {  // 32-token blocks
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (e == 1) {
+        if (r.valid <= 32) {
+#pragma unroll
+          for (int i = 0; i < KB; ++i) r.w[KB + i] = 0u;
+          r.sz[1] = 0u;
+          r.tok2 = r.tok;  // any valid memory: those tokens are hidden
+          break;
+        }
+        rec = record_ptr(L, b, h, p0 / 32 + 1);
+      }
+      const uint32_t* kc = reinterpret_cast<const uint32_t*>(rec + L.kc_off);
+      if constexpr (KB == 2) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(kc + kc_word_index(d, 0, 2)));
+        r.w[2 * e] = v.x, r.w[2 * e + 1] = v.y;
+      } else {
+#pragma unroll
+        for (int c = 0; c < KB / 4; ++c) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(kc + kc_word_index(d, 4 * c, KB)));
+          r.w[KB * e + 4 * c] = v.x, r.w[KB * e + 4 * c + 1] = v.y, r.w[KB * e + 4 * c + 2] = v.z,
+                          r.w[KB * e + 4 * c + 3] = v.w;
+        }
+      }
+      if (L.k_axis == 0) r.sz[e] = __ldg(reinterpret_cast<const uint32_t*>(rec + L.ksz_off) + d);
+      else (e == 0 ? r.tok : r.tok2) = reinterpret_cast<const uint32_t*>(rec + L.ksz_off) + d / L.group_v;
+    }
+  }
+}
+template <int KB>
+__device__ __forceinline__ void store_key_row(const LayerView& L, const KeyRow<KB>& r, uint32_t row, int d) {
+  constexpr int per = 32 / KB, pairs = per / 2;
+  if (r.valid == 0) {
+    zero_row(row);
+  } else if (L.k_axis == 0) {
+    uint32_t s[2], z[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      s[e] = __byte_perm(r.sz[e], r.sz[e], 0x1010);
+      z[e] = __byte_perm(r.sz[e], r.sz[e], 0x3232);
+    }
+    expand_row<KB, false>(r.w, row, d & 7, [&](int pair, uint32_t& s2, uint32_t& z2) {
+      s2 = s[pair >> 4];
+      z2 = z[pair >> 4];
+    });
+  } else {
+    const int ng = kD / L.group_v;
+    expand_row<KB, false>(r.w, row, d & 7, [&](int pair, uint32_t& s2, uint32_t& z2) {
+      const int base = (pair / pairs) * per, a = base + code_at(2 * (pair % pairs), per),
+                c = base + code_at(2 * (pair % pairs) + 1, per);
+      const uint32_t u = __ldg((a < 32 ? r.tok : r.tok2) + (a & 31) * ng);
+      const uint32_t v = __ldg((c < 32 ? r.tok : r.tok2) + (c & 31) * ng);
+      s2 = __byte_perm(u, v, 0x5410);
+      z2 = __byte_perm(u, v, 0x7632);
+    });
+  }
+}
+
+// 64 value codes (channels 64 * cb ..) of the token at position p.
+template <int VB>
+struct ValueRow {
+  uint32_t w[2 * VB];
+  uint32_t sz[2];  // (scale, zero) of the first and second 32 channels
+  bool valid;
+};
+template <int VB>
+__device__ __forceinline__ void load_value_row(const LayerView& L, int b, int h, int p, int q, int cb,
+                                               ValueRow<VB>& r) {
+  r.valid = p < q;
+  if (!r.valid) return;
+  const int G = L.group_k, TT = L.tile_tokens, t = p & (TT - 1), ng = kD / L.group_v;
+  const uint8_t* rec = record_ptr(L, b, h, p / G);
+  const uint8_t* tp = rec + L.tile0_off + (G > 64 ? (int64_t)((p / 64) & 1) * L.tile_bytes : 0);
+  const int row = vc_row(t, TT, L.k_bits);
+  const uint4* vc = reinterpret_cast<const uint4*>(tp + L.vc_off) + row * VB;
+  const int x = chunk_swizzle(row, VB);
+#pragma unroll
+  for (int c = 0; c < VB / 2; ++c) {
+    const uint4 v = __ldg(vc + ((cb * (VB / 2) + c) ^ x));
+    r.w[4 * c] = v.x, r.w[4 * c + 1] = v.y, r.w[4 * c + 2] = v.z, r.w[4 * c + 3] = v.w;
+  }
+  const unsigned short* sz = reinterpret_cast<const unsigned short*>(tp + L.vsz_off);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (e == 1 && L.group_v >= 64) {
+      r.sz[1] = r.sz[0];
+      break;
+    }
+    const int g = (64 * cb + 32 * e) / L.group_v;
+    const int i = vsz_half_index(t, g, TT, L.k_bits, ng, false), j = vsz_half_index(t, g, TT, L.k_bits, ng, true);
+    r.sz[e] = (uint32_t)__ldg(sz + i) | ((uint32_t)__ldg(sz + j) << 16);
+  }
+}
+template <int VB>
+__device__ __forceinline__ void store_value_row(const ValueRow<VB>& r, uint32_t row, int x) {
+  if (!r.valid) {
+    zero_row(row);
+    return;
+  }
+  uint32_t s[2], z[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    s[e] = __byte_perm(r.sz[e], r.sz[e], 0x1010);
+    z[e] = __byte_perm(r.sz[e], r.sz[e], 0x3232);
+  }
+  expand_row<VB, true>(r.w, row, x, [&](int pair, uint32_t& s2, uint32_t& z2) {
+    s2 = s[pair >> 4];
+    z2 = z[pair >> 4];
+  });
+}
+
+struct Bars {
+  uint32_t k_full, k_empty, v_full, v_empty, s_full, p_ready, pv_done, q_ready, drain;  // addresses of arrays of barriers
+};
+
+// Key tiles of phase A: thread kt of 64 expands channels kt and kt + 64 of
+// both 64-token parts of a tile; the next row's codes load while one expands.
+template <int KB>
+__device__ bool produce_keys(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, int kt,
+                             volatile int* abort) {
+  const int end = min(it.k1, it.nA);
+  if (it.k0 >= end) return true;
+  const int units = (end - it.k0) * 4;
+  KeyRow<KB> cur, nxt;
+  auto load = [&](int u, KeyRow<KB>& r) {
+    const int p0 = (it.a0 + it.k0 + (u >> 2)) * kTile + 64 * ((u >> 1) & 1);
+    load_key_row<KB>(p.L, it.b, it.h, p0, it.q, kt + 64 * (u & 1), r);
+  };
+  load(0, nxt);
+  for (int u = 0; u < units; ++u) {
+    cur = nxt;
+    if (u + 1 < units) load(u + 1, nxt);
+    const int c = u >> 2, st = c % kKStages;
+    if ((u & 3) == 0 && c >= kKStages && !mbar_wait_warp(bar.k_empty + 8 * st, ((c / kKStages) - 1) & 1, abort)) return false;
+    const int d = kt + 64 * (u & 1);
+    store_key_row<KB>(p.L, cur, smem + kKOff + st * kTileBytes + ((u >> 1) & 1) * kHalf + d * 128, d);
+    if ((u & 3) == 3) {
+      fence_async_smem();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(bar.k_full + 8 * st);
+    }
+  }
+  return true;
+}
+// Value tiles of phase A: thread vt of 64 expands tokens vt and vt + 64, both
+// 64-channel halves, into the keys' token order.
+template <int VB>
+__device__ bool produce_values(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, int vt,
+                               volatile int* abort) {
+  const int end = min(it.k1, it.nA);
+  if (it.k0 >= end) return true;
+  const int units = (end - it.k0) * 4, per = 32 / p.L.k_bits;
+  const int place = (vt & ~(per - 1)) + place_of(vt & (per - 1), per);
+  ValueRow<VB> cur, nxt;
+  auto load = [&](int u, ValueRow<VB>& r) {
+    const int pos = (it.a0 + it.k0 + (u >> 2)) * kTile + 64 * ((u >> 1) & 1) + vt;
+    load_value_row<VB>(p.L, it.b, it.h, pos, it.q, u & 1, r);
+  };
+  load(0, nxt);
+  for (int u = 0; u < units; ++u) {
+    cur = nxt;
+    if (u + 1 < units) load(u + 1, nxt);
+    const int c = u >> 2, st = c % kVStages;
+    if ((u & 3) == 0 && c >= kVStages && !mbar_wait_warp(bar.v_empty + 8 * st, ((c / kVStages) - 1) & 1, abort)) return false;
+    const int row = 64 * ((u >> 1) & 1) + place;
+    store_value_row<VB>(cur, smem + kVOff + st * kTileBytes + (u & 1) * kHalf + row * 128, row & 7);
+    if ((u & 3) == 3) {
+      fence_async_smem();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(bar.v_full + 8 * st);
+    }
+  }
+  return true;
+}
+// Key or value tiles of phase B: rows of exact tokens, copied as they are
+// (both operands take [64-channel block][token][128 bytes]); entries past the
+// last one that a row sees are zeros.
+template <int STAGES>
+__device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t tiles, uint32_t full, uint32_t empty,
+                              const void* sink, const void* ring, const void* fresh, int kt, volatile int* abort) {
+  const LayerView& L = p.L;
+  const int64_t unit = (int64_t)it.b * L.num_kv_heads + it.h;
+  const uint4* sink_p = reinterpret_cast<const uint4*>(sink) + unit * KVQ_MAX_SINKS * 16;
+  const uint4* ring_p = reinterpret_cast<const uint4*>(ring) + unit * L.residual * 16;
+  const uint4* new_p = reinterpret_cast<const uint4*>(fresh) + ((int64_t)p.in_off[it.i] * L.num_kv_heads + it.h) * 16;
+  const int held = it.s + it.n, last = held + it.t1, ch = kt & 15;
+  const int slot0 = it.q % L.residual;  // ring slot of the first ring token
+  for (int k = max(it.k0, it.nA); k < it.k1; ++k) {
+    const int c = k - it.k0, st = c % STAGES, e0 = it.tile_b(k) * kTile;
+    if (c >= STAGES && !mbar_wait_warp(empty + 8 * st, ((c / STAGES) - 1) & 1, abort)) return false;
+    const uint32_t dst = tiles + st * kTileBytes + (ch >> 3) * kHalf;
+#pragma unroll 8
+    for (int i = 0; i < kTile / 4; ++i) {
+      const int row = (kt >> 4) + 4 * i, e = e0 + row;
+      const uint4* src;
+      if (e >= held) {
+        src = new_p + (int64_t)min(e - held, it.t1) * L.num_kv_heads * 16;
+      } else if (e < it.s) {
+        src = sink_p + e * 16;
+      } else {
+        int slot = slot0 + e - it.s;
+        if (slot >= L.residual) slot -= L.residual;
+        src = ring_p + slot * 16;
+      }
+      cp_async16(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src + ch, e <= last);
+    }
+    asm volatile("cp.async.commit_group;\n cp.async.wait_group 0;" ::: "memory");
+    fence_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(full + 8 * st);
+  }
+  return true;
+}
+
+// ------------------------------------------------------------------- softmax
+// Radix-2 butterflies of one row held by one thread, then 1/sqrt(128): x . H.
+__device__ __forceinline__ void rotate_row(float (&x)[kD]) {
+#pragma unroll
+  for (int w = 1; w < kD; w *= 2)
+#pragma unroll
+    for (int c = 0; c < kD; ++c)
+      if ((c & w) == 0) {
+        const float a = x[c], b = x[c + w];
+        x[c] = a + b;
+        x[c + w] = a - b;
+      }
+  const float s = (float)(1.0 / 11.313708498984761);
+#pragma unroll
+  for (int c = 0; c < kD; ++c) x[c] *= s;
+}
+
+// Writes this thread's query row into its slot's A tile: phase A (fp16, times
+// a power of two, rotated for a Hadamard cache) or phase B (as it is), with
+// the sign of the softmax scale. Returns log2-units per score.
+__device__ __forceinline__ float load_query(const ChunkParams& p, const Item& it, int r, int row, uint32_t tile,
+                                            bool phase_a) {
+  const bool there = r < it.rows;
+  const bool bf16 = p.L.kv_dtype == KVQ_BF16;
+  const int64_t at = (int64_t)(p.in_off[it.i] + r / it.ngr) * p.num_q_heads + it.h * it.ngr + r % it.ngr;
+  const uint4* src = reinterpret_cast<const uint4*>(p.q) + at * 16;
+  const uint32_t dst = tile + row * 128;
+  const float scale = fabsf(p.scale_log2);
+  const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+  if (!phase_a) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const uint4 v = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      sts16(dst + (c >> 3) * kHalf + (((c & 7) ^ (row & 7)) << 4), v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+    }
+    return fmaxf(scale, 1e-37f);  // never 0: a masked score is -inf times this
+  }
+  float x[kD];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const uint4 v = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (bf16) {
+        x[8 * c + 2 * e] = __uint_as_float(w[e] << 16);
+        x[8 * c + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(half2_of(w[e]));
+        x[8 * c + 2 * e] = f.x;
+        x[8 * c + 2 * e + 1] = f.y;
+      }
+    }
+  }
+  if (p.L.hadamard) rotate_row(x);
+  float mx = 0.f;
+#pragma unroll
+  for (int c = 0; c < kD; ++c) mx = fmaxf(mx, fabsf(x[c]));
+  // the row's largest value to [8, 16)
+  const int e = mx > 0.f ? min(100, 3 - ((int)(__float_as_uint(mx) >> 23) - 127)) : 0;
+  const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = pack2<false>(x[8 * c + 2 * j] * up, x[8 * c + 2 * j + 1] * up);
+    sts16(dst + (c >> 3) * kHalf + (((c & 7) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+  }
+  return fmaxf(scale * __uint_as_float((uint32_t)(127 - e) << 23), 1e-37f);
+}
+
+__device__ __forceinline__ void load_o(uint32_t tm_o, float (&x)[kD]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+#pragma unroll
+  for (int c = 0; c < kD; c += 32) tmem_ld32(tm_o + c, r + c);
+#pragma unroll
+  for (int c = 0; c < kD; c += 32) tmem_wait_ld(r + c);
+}
+// Bits [a, b) of a word (bounds outside 0 .. 32 are cut off).
+__device__ __forceinline__ uint32_t bit_range(int a, int b) {
+  const uint32_t below_b = b <= 0 ? 0u : b >= 32 ? 0xffffffffu : (1u << b) - 1u;
+  const uint32_t below_a = a <= 0 ? 0u : a >= 32 ? 0xffffffffu : (1u << a) - 1u;
+  return below_b & ~below_a;
+}
+// Bits in token order to the places of code_at: a perfect shuffle of each
+// group of `per` bits (per = 4: none).
+__device__ __forceinline__ uint32_t shuffle_bits(uint32_t x, int per) {
+  auto swap = [&](uint32_t m, int d) {  // swaps the bits of m with those d above
+    const uint32_t t = (x ^ (x >> d)) & m;
+    x ^= t ^ (t << d);
+  };
+  if (per == 16) swap(0x00f000f0u, 4);
+  if (per >= 8) {
+    swap(0x0c0c0c0cu, 2);
+    swap(0x22222222u, 1);
+  }
+  return x;
+}
+// Scores whose bit is clear become -inf; bits(c) gives those of columns c ..
+// c + 31.
+template <class F>
+__device__ __forceinline__ void mask_scores(uint32_t (&s)[kTile], F bits) {
+#pragma unroll
+  for (int c = 0; c < kTile; c += 32) {
+    const uint32_t m = bits(c);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!((m >> e) & 1u)) s[c + e] = 0xff800000u;
+  }
+}
+
+// Probabilities of one row of a tile: m (log2 units, the value subtracted) and
+// the sum l are the row's state; s becomes packed pairs written to P.
+template <bool BF16>
+__device__ __forceinline__ void write_probs(uint32_t (&s)[kTile], float cs, float bias, float& l, uint32_t tm_s) {
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const float a = ex2(fmaf(__uint_as_float(s[32 * q + 2 * c]), cs, -bias));
+      const float b = ex2(fmaf(__uint_as_float(s[32 * q + 2 * c + 1]), cs, -bias));
+      sum[c & 1] += a;
+      sum[2 + (c & 1)] += b;
+      w[c] = pack2<BF16>(a, b);
+    }
+    tmem_st16(tm_s + 16 * q, w);
+  }
+  l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+__device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32_t smem, uint32_t tmem,
+                             const Bars& bar, volatile int* abort) {
+  const LayerView& L = p.L;
+  const int row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
+  const int r = it.r0 + (it.both ? w * kRows : 0) + row;
+  const int t = min(r, it.rows - 1) / it.ngr;  // the row's new token
+  const bool bf16 = L.kv_dtype == KVQ_BF16;
+  const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+  const uint32_t tm_s = tmem + lanes + kTmemS + w * kTile, tm_o = tmem + lanes + kTmemO + w * kD;
+  const uint32_t qtile = smem + kQOff + w * kTileBytes;
+  const int n = it.slot_tiles(w);
+  float m = -INFINITY, l = 0.f, cs = 0.f;
+  const int per = 32 / L.k_bits;  // key codes per word
+  const int hi_b = it.s + it.n + t;                        // phase B: the row's own entry
+  const int lo_b = p.window > 0 ? hi_b - p.window : -1;     // entries up to this are hidden
+  const int lo_a = p.window > 0 ? it.q + it.n + t - p.window : -1;
+  // tile-uniform: does any row of the item hide something of a tile?
+  const int first_hi = it.s + it.n + it.t0, last_lo_b = p.window > 0 ? it.s + it.n + it.t1 - p.window : -1;
+  const int last_lo_a = p.window > 0 ? it.q + it.n + it.t1 - p.window : -1;
+  for (int j = 0; j < n; ++j) {
+    const int k = it.slot_tile(w, j);
+    const bool in_a = k < it.nA;
+    const bool enter_b = !in_a && (j == 0 || it.slot_tile(w, j - 1) < it.nA);
+    if (j == 0 || enter_b) {
+      if (j > 0) {  // every product of phase A must be in O, and have read Q
+        if (!mbar_wait_warp(bar.pv_done + 8 * w, (j - 1) & 1, abort)) return false;
+        tc_after();
+        if (L.hadamard) {  // O out of the rotated basis
+          float x[kD];
+          load_o(tm_o, x);
+          rotate_row(x);
+#pragma unroll
+          for (int c = 0; c < kD; c += 32) tmem_st32(tm_o + c, reinterpret_cast<const uint32_t*>(x) + c);
+          tmem_wait_st();
+        }
+      }
+      cs = load_query(p, it, r, row, qtile, in_a);
+      fence_async_smem();
+      tc_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(bar.q_ready + 8 * w);
+    }
+    if (!mbar_wait_warp(bar.s_full + 8 * w, j & 1, abort)) return false;
+    tc_after();
+    uint32_t s[kTile];
+#pragma unroll
+    for (int c = 0; c < kTile; c += 32) tmem_ld32(tm_s + c, s + c);
+#pragma unroll
+    for (int c = 0; c < kTile; c += 32) tmem_wait_ld(s + c);
+    if (in_a) {
+      const int p0 = (it.a0 + k) * kTile;
+      if (p0 + kTile > it.q || p0 <= last_lo_a)
+        mask_scores(s, [&](int c) { return shuffle_bits(bit_range(lo_a + 1 - p0 - c, it.q - p0 - c), per); });
+    } else {
+      const int e0 = it.tile_b(k) * kTile;
+      if (e0 + kTile - 1 > first_hi || e0 <= last_lo_b)
+        mask_scores(s, [&](int c) {
+          return bit_range(lo_b + 1 - e0 - c, hi_b + 1 - e0 - c) | bit_range(0, min(it.first_e, hi_b + 1) - e0 - c);
+        });
+    }
+    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int c = 0; c < kTile; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], __uint_as_float(s[c]));
+    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * cs;
+    const bool grow = mx > m + kLazy;
+    if (__any_sync(0xffffffffu, grow)) {
+      // the previous product of this slot is complete: its scores' barrier
+      // completed after it
+      const float mn = grow ? mx : m;
+      const float a = grow ? ex2(m - mn) : 1.f;  // 0 while m = -inf
+      m = mn;
+      l *= a;
+      if (j > 0) {
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(tm_o + c, o);
+          tmem_wait_ld16(o);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+          tmem_st16(tm_o + c, o);
+        }
+      }
+    }
+    const float bias = m == -INFINITY ? 0.f : m - kOffset;
+    if (in_a || !bf16) write_probs<false>(s, cs, bias, l, tm_s);
+    else write_probs<true>(s, cs, bias, l, tm_s);
+    tmem_wait_st();
+    tc_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar.p_ready + 8 * w);
+  }
+  // ---- the row's output or part
+  const bool there = r < it.rows;
+  float x[kD];
+  if (n > 0) {
+    if (!mbar_wait_warp(bar.pv_done + 8 * w, (n - 1) & 1, abort)) return false;
+    tc_after();
+    load_o(tm_o, x);
+    if (L.hadamard && it.slot_tile(w, n - 1) < it.nA) rotate_row(x);
+  } else {
+#pragma unroll
+    for (int c = 0; c < kD; ++c) x[c] = 0.f;
+  }
+  if (!there) return true;
+  if (it.parts > 1) {
+    const int64_t rec = p.part0[it.i] + ((int64_t)it.h * it.rows + r) * it.parts + it.part + (it.both ? 0 : w);
+    float4* o = reinterpret_cast<float4*>(p.ws_o + rec * kD);
+#pragma unroll
+    for (int c = 0; c < kD / 4; ++c) o[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+    p.ws_ml[rec] = make_float2(m, l);
+    return true;
+  }
+  const float f = 1.f / l;  // every row sees its own token
+  const int64_t at = ((int64_t)(p.in_off[it.i] + r / it.ngr) * p.num_q_heads + it.h * it.ngr + r % it.ngr) * kD;
+  if (p.out_dtype == KVQ_F32) {
+    float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at);
+#pragma unroll
+    for (int c = 0; c < kD / 4; ++c)
+      o[c] = make_float4(x[4 * c] * f, x[4 * c + 1] * f, x[4 * c + 2] * f, x[4 * c + 3] * f);
+  } else {
+    uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at);
+    const bool ob = p.out_dtype == KVQ_BF16;
+#pragma unroll
+    for (int c = 0; c < kD / 8; ++c) {
+      uint32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        y[e] = ob ? pack2<true>(x[8 * c + 2 * e] * f, x[8 * c + 2 * e + 1] * f)
+                  : pack2<false>(x[8 * c + 2 * e] * f, x[8 * c + 2 * e + 1] * f);
+      o[c] = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  }
+  return true;
+}
+
+// One thread issues every product of the item, in the order S(0), S(1), then
+// P V of step v and S of step v + 2: a slot's next scores are queued behind
+// its own product (which reads the P they overwrite) while the other slot's
+// softmax runs.
+__device__ bool issue_products(const ChunkParams& p, const Item& it, uint32_t smem, uint32_t tmem, const Bars& bar,
+                               volatile int* abort) {
+  const int steps = it.steps();
+  const bool bf16 = p.L.kv_dtype == KVQ_BF16;
+  auto scores = [&](int v) -> bool {
+    const int w = v & 1, c = it.both ? v >> 1 : v, k = it.k0 + c, st = c % kKStages;
+    const bool in_a = k < it.nA;
+    const int j = v >> 1;
+    const bool enter_b = !in_a && (j == 0 || it.slot_tile(w, j - 1) < it.nA);
+    if (j == 0 || enter_b) {
+      if (!mbar_wait(bar.q_ready + 8 * w, j == 0 ? 0 : 1, abort)) return false;
+      tc_after();
+    }
+    if ((!it.both || w == 0) && !mbar_wait(bar.k_full + 8 * st, (c / kKStages) & 1, abort)) return false;
+    tc_after();
+    const uint32_t q = smem + kQOff + w * kTileBytes, kt = smem + kKOff + st * kTileBytes;
+    const uint32_t d = tmem + kTmemS + w * kTile;
+    const uint32_t id = inst_desc(!in_a && bf16, in_a);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint64_t a = desc_k(q + (e >> 2) * kHalf + (e & 3) * 32);
+      const uint64_t b = in_a ? desc_mn(kt + e * 2048) : desc_k(kt + (e >> 2) * kHalf + (e & 3) * 32);
+      mma_ss(d, a, b, id, e > 0);
+    }
+    tc_commit(bar.s_full + 8 * w);
+    if (!it.both || w == 1) tc_commit(bar.k_empty + 8 * st);
+    return true;
+  };
+  auto values = [&](int v) -> bool {
+    const int w = v & 1, c = it.both ? v >> 1 : v, k = it.k0 + c, st = c % kVStages, j = v >> 1;
+    if (!mbar_wait(bar.p_ready + 8 * w, j & 1, abort)) return false;
+    if ((!it.both || w == 0) && !mbar_wait(bar.v_full + 8 * st, (c / kVStages) & 1, abort)) return false;
+    tc_after();
+    const uint32_t vt = smem + kVOff + st * kTileBytes;
+    const uint32_t pa = tmem + kTmemS + w * kTile, d = tmem + kTmemO + w * kD;
+    const uint32_t id = inst_desc(k >= it.nA && bf16, true);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mma_ts(d, pa + 8 * e, desc_mn(vt + e * 2048), id, j > 0 || e > 0);
+    tc_commit(bar.pv_done + 8 * w);
+    if (!it.both || w == 1) tc_commit(bar.v_empty + 8 * st);
+    return true;
+  };
+  for (int v = 0; v < 2 && v < steps; ++v)
+    if (!scores(v)) return false;
+  for (int v = 0; v < steps; ++v) {
+    if (!values(v)) return false;
+    if (v + 2 < steps && !scores(v + 2)) return false;
+  }
+  return true;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_constant__ ChunkParams p) {
+  extern __shared__ uint8_t raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const uint32_t smem = (smem_u32(raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5;
+  volatile int* abort = &s_abort;
+  Bars bar;
+  {
+    uint32_t at = smem + kBarOff;
+    bar.k_full = at, at += 8 * kKStages;
+    bar.k_empty = at, at += 8 * kKStages;
+    bar.v_full = at, at += 8 * kVStages;
+    bar.v_empty = at, at += 8 * kVStages;
+    bar.s_full = at, at += 16;
+    bar.p_ready = at, at += 16;
+    bar.pv_done = at, at += 16;
+    bar.q_ready = at, at += 16;
+    bar.drain = at;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(bar.k_full + 8 * i, 2);
+      mbar_init(bar.k_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(bar.v_full + 8 * i, 2);
+      mbar_init(bar.v_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar.s_full + 8 * i, 1);
+      mbar_init(bar.p_ready + 8 * i, 4);
+      mbar_init(bar.pv_done + 8 * i, 1);
+      mbar_init(bar.q_ready + 8 * i, 4);
+    }
+    mbar_init(bar.drain, 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = s_tmem;
+  const Item it = find_item(p, blockIdx.x);
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    (void)softmax_slot(p, it, warp >> 2, smem, tmem, bar, abort);
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    const LayerView& L = p.L;
+    const int kt = threadIdx.x & 63;
+    if (warp < 10) {
+      const bool ok = L.k_bits == 2   ? produce_keys<2>(p, it, smem, bar, kt, abort)
+                      : L.k_bits == 4 ? produce_keys<4>(p, it, smem, bar, kt, abort)
+                                      : produce_keys<8>(p, it, smem, bar, kt, abort);
+      if (ok)
+        (void)produce_exact<kKStages>(p, it, smem + kKOff, bar.k_full, bar.k_empty, L.sink_k, L.ring_k, p.k, kt, abort);
+    } else {
+      const bool ok = L.v_bits == 2   ? produce_values<2>(p, it, smem, bar, kt, abort)
+                      : L.v_bits == 4 ? produce_values<4>(p, it, smem, bar, kt, abort)
+                                      : produce_values<8>(p, it, smem, bar, kt, abort);
+      if (ok)
+        (void)produce_exact<kVStages>(p, it, smem + kVOff, bar.v_full, bar.v_empty, L.sink_v, L.ring_v, p.v, kt, abort);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 12 && (threadIdx.x & 31) == 0) {
+      if (!issue_products(p, it, smem, tmem, bar, abort)) {
+        // let the products in flight finish before the tensor memory goes
+        tc_commit(bar.drain);
+        const long long t0 = clock64();
+        while (!mbar_try(bar.drain, 0) && clock64() - t0 < kWaitCycles) {
+        }
+      }
+    }
+    __syncwarp();
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 12)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (threadIdx.x == 0 && s_abort) atomicOr(p.err, 1);
+}
+
+// Merges the parts of a row (parts > 1): a warp per row, four channels a lane.
+constexpr int kCombineWarps = 8;
+__global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(const __grid_constant__ ChunkParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t g = (int64_t)blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+  if (g >= p.merge_rows) return;
+  int lo = 0, hi = p.nseq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.merge0[mid] <= g) lo = mid;
+    else hi = mid - 1;
+  }
+  const int i = lo, ngr = p.num_q_heads / p.L.num_kv_heads, rows = p.t_new[i] * ngr;
+  const int parts = chunk_parts(p.splits[i]);
+  const int64_t x = g - p.merge0[i];  // h * rows + r
+  const int64_t rec = p.part0[i] + x * parts;
+  float M = -INFINITY;
+  for (int e = lane; e < parts; e += 32) M = fmaxf(M, p.ws_ml[rec + e].x);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int e = 0; e < parts; ++e) {
+    const float2 ml = p.ws_ml[rec + e];
+    const float4 v = reinterpret_cast<const float4*>(p.ws_o + (rec + e) * kD)[lane];
+    const float f = ex2(ml.x - M);  // 0 for a part that saw nothing
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+    l = fmaf(f, ml.y, l);
+  }
+  const float f = 1.f / l;
+  const int h = (int)(x / rows), r = (int)(x % rows);
+  const int64_t at = ((int64_t)(p.in_off[i] + r / ngr) * p.num_q_heads + h * ngr + r % ngr) * kD + 4 * lane;
+  if (p.out_dtype == KVQ_F32) {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at) =
+        make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+  } else {
+    const bool ob = p.out_dtype == KVQ_BF16;
+    const uint32_t a = ob ? pack2<true>(acc.x * f, acc.y * f) : pack2<false>(acc.x * f, acc.y * f);
+    const uint32_t c = ob ? pack2<true>(acc.z * f, acc.w * f) : pack2<false>(acc.z * f, acc.w * f);
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + at) = make_uint2(a, c);
+  }
+}
+
+}  // namespace
+
+bool chunk_tc_supported(const LayerView& L) { return L.residual_v == L.residual; }
+
+cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream) {
+  if (p.items <= 0) return cudaSuccess;
+  // (set on every launch: it is per device, and a few hundred nanoseconds)
+  cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  chunk_tc_kernel<<<p.items, kThreads, kSmemBytes, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.merge_rows == 0) return e;
+  chunk_combine_kernel<<<(unsigned)((p.merge_rows + kCombineWarps - 1) / kCombineWarps), 32 * kCombineWarps, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace kvq

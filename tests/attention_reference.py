@@ -27,7 +27,8 @@ def attend(q, k, v, first, scale, window=0, sinks=0):
     """Queries q [T, Hq, D] of the tokens first, first + 1, ... over tokens k, v [n, Hkv, D]: query t sees token j
     when j <= first + t and, with a window, when also j > first + t - window or j < sinks. A token that is not seen
     takes no part, whatever it holds. Returns (out [T, Hq, D], sum_j p_j |v_j| [T, Hq, D], max_j sum_d |q_d k_jd| over
-    seen tokens [T, Hq, 1]), in 64 bits."""
+    seen tokens [T, Hq, 1], and the same two with 2-norms of whole vectors, sum_j p_j |v_j|_2 and max_j |q|_2 |k_j|_2
+    [T, Hq, 1]), in 64 bits."""
     q = q.double()
     T, Hq, D = q.shape
     n, Hkv, _ = k.shape
@@ -41,7 +42,8 @@ def attend(q, k, v, first, scale, window=0, sinks=0):
     k, v, seen = k[some], v[some], seen[:, some]
     if k.shape[0] == 0:
         z = torch.zeros_like(q)
-        return z, z.clone(), torch.zeros(T, Hq, 1, device=q.device, dtype=torch.float64)
+        o = torch.zeros(T, Hq, 1, device=q.device, dtype=torch.float64)
+        return z, z.clone(), o, o.clone(), o.clone()
     qh = q.reshape(T, Hkv, g, D)
     z = torch.einsum("thgd,nhd->thgn", qh, k) * scale
     z = z.masked_fill(~seen[:, None, None, :], float("-inf"))
@@ -49,10 +51,12 @@ def attend(q, k, v, first, scale, window=0, sinks=0):
     size = torch.einsum("thgd,nhd->thgn", qh.abs(), k.abs()).masked_fill(~seen[:, None, None, :], 0.0)
     out = torch.einsum("thgn,nhd->thgd", p, v)
     mean = torch.einsum("thgn,nhd->thgd", p, v.abs())
-    return out.reshape(T, Hq, D), mean.reshape(T, Hq, D), size.amax(-1, keepdim=True).reshape(T, Hq, 1)
+    norms = torch.einsum("thgn,nh->thg", p, v.norm(dim=-1)).reshape(T, Hq, 1)
+    most = (qh.norm(dim=-1) * k.norm(dim=-1).amax(0)[None, :, None]).reshape(T, Hq, 1)
+    return out.reshape(T, Hq, D), mean.reshape(T, Hq, D), size.amax(-1, keepdim=True).reshape(T, Hq, 1), norms, most
 
 
-def bound(out, mean, size, scale, cfg, out_dtype):
+def bound(ref, scale, cfg, out_dtype):
     """Largest error of the tensor-core kernels' outputs, element by element.
 
     * A dequantized key is rounded to fp16 (relative 2^-11), and so is a rotated query: each score is off by at
@@ -63,18 +67,25 @@ def bound(out, mean, size, scale, cfg, out_dtype):
     * fp32 sums: 1e-5 relative to the mean of |v| covers the 128-term dot products (128 * 2^-24) and the sums over
       tokens, which add in blocks.
     * The output is rounded once: half a step of its type.
+    * A Hadamard cache rounds in the rotated basis: a score is off by at most e with sum|(Hq)_d (Hk)_d| <= |q|_2 |k|_2
+      in the place of sum|q k| (Cauchy-Schwarz, H orthogonal), and a value element, errors u |(Hv)_d| rotated back with
+      entries 1/sqrt(D), by at most u / sqrt(D) sum_d |(Hv)_d| <= u |v|_2. The norms of a row's visible tokens bound both.
     """
+    out, mean, size, norms, most = ref
+    if cfg.hadamard:
+        size = most
     e = abs(scale) * 2.0 ** -10 * size
     weights = torch.expm1(2.0 * e)
     p = 2.0 ** -8 if cfg.kv_dtype == torch.bfloat16 else 2.0 ** -11
-    err = mean * (weights + p + 2.0 ** -11 + 1e-5) + 1e-5
+    rounded = norms if cfg.hadamard else mean
+    err = mean * (weights + p) + rounded * (2.0 ** -11 + 1e-5) + 1e-5
     return err + (out.abs() + err) * torch.finfo(out_dtype).eps / 2
 
 
 def assert_within(got, ref, scale, cfg, what=""):
-    out, mean, size = ref
+    out = ref[0]
     assert got.shape == out.shape, (got.shape, out.shape)
     err = (got.double() - out).abs()
-    tol = bound(out, mean, size, scale, cfg, got.dtype)
+    tol = bound(ref, scale, cfg, got.dtype)
     worst = (err / tol).max().item() if err.numel() else 0.0
     assert worst <= 1.0, f"{what}: error is {worst:.3g} of what the roundings allow (max abs {err.max().item():.3g})"
