@@ -1161,6 +1161,7 @@ kvq_status kvq_chunk_attention(kvq_cache* c, int32_t layer, const void* k, const
   p.num_q_heads = cfg.num_q_heads;
   p.window = window;
   p.sink_tokens = cfg.sink_tokens;
+  p.tokens = (int32_t)total;
   p.nseq = 0;
   int32_t off = 0;
   for (int b = 0; b < batch; ++b) {

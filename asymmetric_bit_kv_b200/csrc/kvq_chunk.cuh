@@ -25,6 +25,7 @@ struct ChunkParams {
   int32_t num_q_heads;
   int32_t window;       // 0: none
   int32_t sink_tokens;  // S of the cache: tokens that stay visible outside the window
+  int32_t tokens;       // rows of k and v
   int32_t nseq;         // entries of the tables
   int32_t items;        // work items of all entries
   int32_t seq[KVQ_MAX_BATCH];

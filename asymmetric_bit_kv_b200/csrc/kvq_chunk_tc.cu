@@ -19,9 +19,12 @@
 // parts are merged by chunk_combine_kernel.
 //
 // Warps: 0-3 and 4-7 the softmax of slots 0 and 1 (a thread owns a row, so
-// maxima, sums and the rotation of a row need no exchange), 8-9 key tiles,
-// 10-11 value tiles, 12 issues the MMAs. Registers move from the producers to
-// the softmax warps (setmaxnreg: 184 + 184 + 88 + 56 = 4 x 128).
+// maxima, sums and the rotation of a row need no exchange), 8-11 key tiles,
+// 12-15 value tiles, 16 issues the MMAs (17-19 idle: registers move between
+// whole warpgroups, setmaxnreg 144 + 144 + 72 + 72 + 48 = 5 x 96). The hot
+// loops are kept short (32 columns, one row of codes at a time): four roles
+// share an SM's instruction caches, and unrolled whole tiles spent most of
+// their time waiting for instructions.
 //
 // Operands. Phase A: codes become fp16 in three instructions per pair (mask
 // into the mantissa of 1024, subtract, one fma q*d + m: the only rounding).
@@ -33,13 +36,15 @@
 // Queries are scaled by a power of two per row (exact but for
 // subnormals), so that any bf16 query fits fp16. Phase B: keys, values,
 // queries and probabilities in the kv dtype, keys K-major.
-// Softmax: probabilities are 2^(z - m + 8) with m raised only when a row's
-// maximum grows by more than 4 (log2 units): O is rescaled rarely, and fp16
-// probabilities keep 14 + 8 binary orders below the maximum before they turn
-// subnormal.
+// Softmax: probabilities are 2^(z - m + 8) with m a whole number that is raised
+// only when a row's maximum passes it by more than 4 (log2 units): one pass over the
+// scores, rescaling of O and of what the tile has written rare and exact (powers of two), and fp16
+// probabilities keep 14 + 8 binary orders below m before they turn subnormal.
 //
 // Every wait is bounded (~2 s): a thread that gives up sets the device error
 // word and an abort flag that ends the others' waits.
+#include <cuda.h>
+
 #include <algorithm>
 
 #include "kvq_chunk.cuh"
@@ -49,7 +54,8 @@ namespace kvq {
 namespace {
 
 constexpr int kRows = kChunkSlotRows, kTile = kChunkTile, kD = kHeadDim;
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
+constexpr int kProducers = 128;  // threads of the key warps, and of the value warps
 constexpr int kKStages = 2, kVStages = 3;
 constexpr int kTileBytes = kTile * kD * 2;
 constexpr int kHalf = kTileBytes / 2;  // one 64-wide block of a tile: 128 rows of 128 bytes
@@ -213,6 +219,12 @@ __device__ __forceinline__ uint32_t inst_desc(bool bf16, bool b_mn) {
          ((uint32_t)(kRows >> 4) << 24);
 }
 
+// The chunk's keys and values as matrices [tokens][Hkv * D], boxes of 128
+// tokens x 64 channels with the 128-byte swizzle.
+struct alignas(64) ChunkMaps {
+  CUtensorMap k, v;
+};
+
 // ------------------------------------------------------------------ the item
 struct Item {
   int i, b, h;          // table entry, sequence, KV head
@@ -345,147 +357,126 @@ __device__ __forceinline__ void zero_row(uint32_t row) {
   for (int c = 0; c < 8; ++c) sts16(row + (c << 4), 0u, 0u, 0u, 0u);
 }
 
-// 64 key codes of channel d at positions p0 .. p0 + 63 (p0 a multiple of 64),
-// in token order, with the scales of their one or two blocks.
+// A block record by its index, and by the index of its 64-token part (with
+// 32-token blocks: the part's first block).
+struct Records {
+  const uint8_t* base;   // contiguous: the unit's first record; paged: the pool
+  const int32_t* table;  // paged: the sequence's row of the page table
+  int64_t bytes;
+  uint32_t per_page, hkv, h;
+  int lg_part;  // log2(64-token parts per block); -1: two blocks per part
+  int tile0, tile_bytes;
+  __device__ __forceinline__ Records(const LayerView& L, int b, int h_) {
+    table = L.page_table ? L.page_table + (int64_t)b * L.max_pages : nullptr;
+    bytes = L.record_bytes;
+    per_page = (uint32_t)L.page_blocks;
+    hkv = (uint32_t)L.num_kv_heads;
+    h = (uint32_t)h_;
+    base = table ? L.blocks : L.blocks + ((int64_t)b * L.num_kv_heads + h_) * L.max_blocks * bytes;
+    lg_part = L.group_k == 128 ? 1 : L.group_k == 64 ? 0 : -1;
+    tile0 = L.tile0_off;
+    tile_bytes = L.tile_bytes;
+  }
+  __device__ __forceinline__ const uint8_t* block(uint32_t j) const {
+    if (!table) return base + j * bytes;
+    const uint32_t run = j / per_page;
+    return base + (((int64_t)__ldg(table + run) * hkv + h) * per_page + (j - run * per_page)) * bytes;
+  }
+  __device__ __forceinline__ int block_of(int part) const { return lg_part < 0 ? 2 * part : part >> lg_part; }
+  // byte offset of a part's tile in its record
+  __device__ __forceinline__ int tile_of(int part) const { return tile0 + (lg_part == 1 ? (part & 1) * tile_bytes : 0); }
+};
+
+// 64 key codes of one channel in token order, with the scales of their one or
+// two blocks.
 template <int KB>
 struct KeyRow {
   uint32_t w[2 * KB];
-  uint32_t sz[2];     // per channel: (scale, zero) of tokens 0-31 and 32-63
-  const uint32_t* tok;  // per token: (scale, zero) pairs of the channel's group, first block
-  const uint32_t* tok2;
-  int valid;          // tokens present: 0, 32 or 64
+  uint32_t sz[2];  // per channel: (scale, zero) of tokens 0-31 and 32-63
+};
+// What a producer thread keeps per channel: byte offsets inside a tile.
+struct KeyChannel {
+  int codes, x;    // the channel's row, its chunk swizzle
+  int sz;          // per channel: its (scale, zero) pair in the record or tile
 };
 template <int KB>
-__device__ __forceinline__ void load_key_row(const LayerView& L, int b, int h, int p0, int q, int d, KeyRow<KB>& r) {
-  r.valid = min(64, max(0, q - p0));
-  if (r.valid == 0) return;
-  const int G = L.group_k;
-  const uint8_t* rec = record_ptr(L, b, h, p0 / G);
-  if (G >= 64) {
-    const uint8_t* tp = rec + L.tile0_off + (G > 64 ? (int64_t)((p0 / 64) & 1) * L.tile_bytes : 0);
-    const uint4* kc = reinterpret_cast<const uint4*>(tp + L.kc_off) + d * (KB / 2);
-    const int x = chunk_swizzle(d, KB / 2);
+__device__ __forceinline__ KeyChannel key_channel(const LayerView& L, int d) {
+  KeyChannel c;
+  const bool wide = L.group_k >= 64;
+  c.x = wide ? chunk_swizzle(d, KB / 2) : KB == 8 ? chunk_swizzle(d, 2) : 0;
+  c.codes = L.kc_off + 4 * (wide ? d * 2 * KB : KB == 2 ? kc_word_index(d, 0, 2) : d * KB);
+  c.sz = (L.rec_ksz_off >= 0 ? L.rec_ksz_off - L.tile0_off : L.ksz_off) + 4 * d;
+  return c;
+}
+// Loads a row of part `part`; `valid` tokens of it exist (0, 32 or 64).
+template <int KB>
+__device__ __forceinline__ void load_key_row(const Records& rec, int part, int valid, const KeyChannel& c, bool axis0,
+                                             KeyRow<KB>& r) {
+  if (valid <= 0) return;
+  if (rec.lg_part >= 0) {
+    const uint8_t* record = rec.block(rec.block_of(part));
+    const uint8_t* tp = record + rec.tile_of(part);
+    const uint4* kc = reinterpret_cast<const uint4*>(tp + c.codes);
 #pragma unroll
-    for (int c = 0; c < KB / 2; ++c) {
-      const uint4 v = __ldg(kc + (c ^ x));
-      r.w[4 * c] = v.x, r.w[4 * c + 1] = v.y, r.w[4 * c + 2] = v.z, r.w[4 * c + 3] = v.w;
+    for (int e = 0; e < KB / 2; ++e) {
+      const uint4 v = __ldg(kc + (e ^ c.x));
+      r.w[4 * e] = v.x, r.w[4 * e + 1] = v.y, r.w[4 * e + 2] = v.z, r.w[4 * e + 3] = v.w;
     }
-    if (L.k_axis == 0) {
-      const uint8_t* k = L.rec_ksz_off >= 0 ? rec + L.rec_ksz_off : tp + L.ksz_off;
-      r.sz[0] = r.sz[1] = __ldg(reinterpret_cast<const uint32_t*>(k) + d);
-    } else {
-      r.tok = reinterpret_cast<const uint32_t*>(tp + L.ksz_off) + d / L.group_v;
-      r.tok2 = r.tok + 32 * (kD / L.group_v);
-    }
-  } else {  // 32-token blocks
+    // (a record's shared scales sit at a fixed place before its first tile)
+    if (axis0) r.sz[0] = __ldg(reinterpret_cast<const uint32_t*>((rec.lg_part == 1 ? record + rec.tile0 : tp) + c.sz));
+    r.sz[1] = r.sz[0];
+  } else {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      if (e == 1) {
-        if (r.valid <= 32) {
+      if (e == 1 && valid <= 32) {
 #pragma unroll
-          for (int i = 0; i < KB; ++i) r.w[KB + i] = 0u;
-          r.sz[1] = 0u;
-          r.tok2 = r.tok;  // any valid memory: those tokens are hidden
-          break;
-        }
-        rec = record_ptr(L, b, h, p0 / 32 + 1);
+        for (int i = 0; i < KB; ++i) r.w[KB + i] = 0u;
+        r.sz[1] = 0u;
+        break;
       }
-      const uint32_t* kc = reinterpret_cast<const uint32_t*>(rec + L.kc_off);
+      const uint8_t* tp = rec.block(rec.block_of(part) + e);
       if constexpr (KB == 2) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(kc + kc_word_index(d, 0, 2)));
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(tp + c.codes));
         r.w[2 * e] = v.x, r.w[2 * e + 1] = v.y;
       } else {
 #pragma unroll
-        for (int c = 0; c < KB / 4; ++c) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(kc + kc_word_index(d, 4 * c, KB)));
-          r.w[KB * e + 4 * c] = v.x, r.w[KB * e + 4 * c + 1] = v.y, r.w[KB * e + 4 * c + 2] = v.z,
-                          r.w[KB * e + 4 * c + 3] = v.w;
+        for (int i = 0; i < KB / 4; ++i) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(tp + c.codes) + (i ^ c.x));
+          r.w[KB * e + 4 * i] = v.x, r.w[KB * e + 4 * i + 1] = v.y, r.w[KB * e + 4 * i + 2] = v.z,
+                          r.w[KB * e + 4 * i + 3] = v.w;
         }
       }
-      if (L.k_axis == 0) r.sz[e] = __ldg(reinterpret_cast<const uint32_t*>(rec + L.ksz_off) + d);
-      else (e == 0 ? r.tok : r.tok2) = reinterpret_cast<const uint32_t*>(rec + L.ksz_off) + d / L.group_v;
+      if (axis0) r.sz[e] = __ldg(reinterpret_cast<const uint32_t*>(tp + c.sz));
     }
   }
 }
+// Per-channel keys.
 template <int KB>
-__device__ __forceinline__ void store_key_row(const LayerView& L, const KeyRow<KB>& r, uint32_t row, int d) {
-  constexpr int per = 32 / KB, pairs = per / 2;
-  if (r.valid == 0) {
-    zero_row(row);
-  } else if (L.k_axis == 0) {
-    uint32_t s[2], z[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      s[e] = __byte_perm(r.sz[e], r.sz[e], 0x1010);
-      z[e] = __byte_perm(r.sz[e], r.sz[e], 0x3232);
-    }
-    expand_row<KB, false>(r.w, row, d & 7, [&](int pair, uint32_t& s2, uint32_t& z2) {
-      s2 = s[pair >> 4];
-      z2 = z[pair >> 4];
-    });
-  } else {
-    const int ng = kD / L.group_v;
-    expand_row<KB, false>(r.w, row, d & 7, [&](int pair, uint32_t& s2, uint32_t& z2) {
-      const int base = (pair / pairs) * per, a = base + code_at(2 * (pair % pairs), per),
-                c = base + code_at(2 * (pair % pairs) + 1, per);
-      const uint32_t u = __ldg((a < 32 ? r.tok : r.tok2) + (a & 31) * ng);
-      const uint32_t v = __ldg((c < 32 ? r.tok : r.tok2) + (c & 31) * ng);
-      s2 = __byte_perm(u, v, 0x5410);
-      z2 = __byte_perm(u, v, 0x7632);
-    });
-  }
-}
-
-// 64 value codes (channels 64 * cb ..) of the token at position p.
-template <int VB>
-struct ValueRow {
-  uint32_t w[2 * VB];
-  uint32_t sz[2];  // (scale, zero) of the first and second 32 channels
-  bool valid;
-};
-template <int VB>
-__device__ __forceinline__ void load_value_row(const LayerView& L, int b, int h, int p, int q, int cb,
-                                               ValueRow<VB>& r) {
-  r.valid = p < q;
-  if (!r.valid) return;
-  const int G = L.group_k, TT = L.tile_tokens, t = p & (TT - 1), ng = kD / L.group_v;
-  const uint8_t* rec = record_ptr(L, b, h, p / G);
-  const uint8_t* tp = rec + L.tile0_off + (G > 64 ? (int64_t)((p / 64) & 1) * L.tile_bytes : 0);
-  const int row = vc_row(t, TT, L.k_bits);
-  const uint4* vc = reinterpret_cast<const uint4*>(tp + L.vc_off) + row * VB;
-  const int x = chunk_swizzle(row, VB);
-#pragma unroll
-  for (int c = 0; c < VB / 2; ++c) {
-    const uint4 v = __ldg(vc + ((cb * (VB / 2) + c) ^ x));
-    r.w[4 * c] = v.x, r.w[4 * c + 1] = v.y, r.w[4 * c + 2] = v.z, r.w[4 * c + 3] = v.w;
-  }
-  const unsigned short* sz = reinterpret_cast<const unsigned short*>(tp + L.vsz_off);
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    if (e == 1 && L.group_v >= 64) {
-      r.sz[1] = r.sz[0];
-      break;
-    }
-    const int g = (64 * cb + 32 * e) / L.group_v;
-    const int i = vsz_half_index(t, g, TT, L.k_bits, ng, false), j = vsz_half_index(t, g, TT, L.k_bits, ng, true);
-    r.sz[e] = (uint32_t)__ldg(sz + i) | ((uint32_t)__ldg(sz + j) << 16);
-  }
-}
-template <int VB>
-__device__ __forceinline__ void store_value_row(const ValueRow<VB>& r, uint32_t row, int x) {
-  if (!r.valid) {
-    zero_row(row);
-    return;
-  }
+__device__ __forceinline__ void store_key_row(const KeyRow<KB>& r, uint32_t row, int d) {
   uint32_t s[2], z[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     s[e] = __byte_perm(r.sz[e], r.sz[e], 0x1010);
     z[e] = __byte_perm(r.sz[e], r.sz[e], 0x3232);
   }
-  expand_row<VB, true>(r.w, row, x, [&](int pair, uint32_t& s2, uint32_t& z2) {
+  expand_row<KB, false>(r.w, row, d & 7, [&](int pair, uint32_t& s2, uint32_t& z2) {
     s2 = s[pair >> 4];
     z2 = z[pair >> 4];
+  });
+}
+// Per-token keys: the (scale, zero) pairs of the channel's group, of tokens 0
+// .. 31 at tok and 32 .. 63 at tok2, are the same for every lane.
+template <int KB>
+__device__ __forceinline__ void store_key_row_per_token(const KeyRow<KB>& r, uint32_t row, int d, const uint8_t* tok,
+                                                        const uint8_t* tok2, int stride) {
+  constexpr int per = 32 / KB, pairs = per / 2;
+  expand_row<KB, false>(r.w, row, d & 7, [&](int pair, uint32_t& s2, uint32_t& z2) {
+    const int base = (pair / pairs) * per, a = base + code_at(2 * (pair % pairs), per),
+              c = base + code_at(2 * (pair % pairs) + 1, per);
+    const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>((a < 32 ? tok : tok2) + (a & 31) * stride));
+    const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>((c < 32 ? tok : tok2) + (c & 31) * stride));
+    s2 = __byte_perm(u, v, 0x5410);
+    z2 = __byte_perm(u, v, 0x7632);
   });
 }
 
@@ -493,28 +484,46 @@ struct Bars {
   uint32_t k_full, k_empty, v_full, v_empty, s_full, p_ready, pv_done, q_ready, drain;  // addresses of arrays of barriers
 };
 
-// Key tiles of phase A: thread kt of 64 expands channels kt and kt + 64 of
-// both 64-token parts of a tile; the next row's codes load while one expands.
+// Key tiles of phase A: thread kt expands channel kt of both 64-token parts of
+// a tile. A row's codes are loaded kAhead rows before they are expanded.
 template <int KB>
 __device__ bool produce_keys(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, int kt,
                              volatile int* abort) {
-  const int end = min(it.k1, it.nA);
-  if (it.k0 >= end) return true;
-  const int units = (end - it.k0) * 4;
-  KeyRow<KB> cur, nxt;
+  const int tiles = min(it.k1, it.nA) - it.k0;
+  if (tiles <= 0) return true;
+  constexpr int kAhead = KB == 8 ? 1 : 2;
+  const Records rec(p.L, it.b, it.h);
+  const bool axis0 = p.L.k_axis == 0;
+  const KeyChannel ch = key_channel<KB>(p.L, kt);
+  const int part0 = 2 * (it.a0 + it.k0), rows = 2 * tiles;
+  KeyRow<KB> buf[kAhead + 1];
   auto load = [&](int u, KeyRow<KB>& r) {
-    const int p0 = (it.a0 + it.k0 + (u >> 2)) * kTile + 64 * ((u >> 1) & 1);
-    load_key_row<KB>(p.L, it.b, it.h, p0, it.q, kt + 64 * (u & 1), r);
+    load_key_row<KB>(rec, part0 + u, u < rows ? it.q - 64 * (part0 + u) : 0, ch, axis0, r);
   };
-  load(0, nxt);
-  for (int u = 0; u < units; ++u) {
-    cur = nxt;
-    if (u + 1 < units) load(u + 1, nxt);
-    const int c = u >> 2, st = c % kKStages;
-    if ((u & 3) == 0 && c >= kKStages && !mbar_wait_warp(bar.k_empty + 8 * st, ((c / kKStages) - 1) & 1, abort)) return false;
-    const int d = kt + 64 * (u & 1);
-    store_key_row<KB>(p.L, cur, smem + kKOff + st * kTileBytes + ((u >> 1) & 1) * kHalf + d * 128, d);
-    if ((u & 3) == 3) {
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) load(a, buf[a + 1]);
+#pragma unroll 1
+  for (int u = 0; u < rows; ++u) {
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) buf[a] = buf[a + 1];
+    load(u + kAhead, buf[kAhead]);
+    const int c = u >> 1, st = c % kKStages, part = part0 + u, valid = it.q - 64 * part;
+    if ((u & 1) == 0 && c >= kKStages && !mbar_wait_warp(bar.k_empty + 8 * st, ((c / kKStages) - 1) & 1, abort))
+      return false;
+    const uint32_t row = smem + kKOff + st * kTileBytes + (u & 1) * kHalf + kt * 128;
+    if (valid <= 0) {
+      zero_row(row);
+    } else if (axis0) {
+      store_key_row<KB>(buf[0], row, kt);
+    } else {
+      const int stride = 4 * (kD / p.L.group_v), at = p.L.ksz_off + 4 * (kt / p.L.group_v);
+      const uint8_t* tok = rec.block(rec.block_of(part)) + rec.tile_of(part) + at;
+      const uint8_t* tok2 = rec.lg_part >= 0 ? tok + 32 * stride
+                            : valid > 32     ? rec.block(rec.block_of(part) + 1) + at
+                                             : tok;
+      store_key_row_per_token<KB>(buf[0], row, kt, tok, tok2, stride);
+    }
+    if (u & 1) {
       fence_async_smem();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive(bar.k_full + 8 * st);
@@ -522,29 +531,81 @@ __device__ bool produce_keys(const ChunkParams& p, const Item& it, uint32_t smem
   }
   return true;
 }
-// Value tiles of phase A: thread vt of 64 expands tokens vt and vt + 64, both
-// 64-channel halves, into the keys' token order.
+
+// 64 value codes (channels 64 * half ..) of one token.
+template <int VB>
+struct ValueRow {
+  uint32_t w[2 * VB];
+  uint32_t sz[2];  // (scale, zero) of the first and second 32 channels
+};
+// Value tiles of phase A: thread vt expands token vt of a tile, both 64-channel
+// halves, into the keys' token order. Loads as for the keys.
 template <int VB>
 __device__ bool produce_values(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, int vt,
                                volatile int* abort) {
-  const int end = min(it.k1, it.nA);
-  if (it.k0 >= end) return true;
-  const int units = (end - it.k0) * 4, per = 32 / p.L.k_bits;
+  const int tiles = min(it.k1, it.nA) - it.k0;
+  if (tiles <= 0) return true;
+  constexpr int kAhead = VB == 8 ? 1 : 2;
+  const LayerView& L = p.L;
+  const Records rec(L, it.b, it.h);
+  const int per = 32 / L.k_bits;
   const int place = (vt & ~(per - 1)) + place_of(vt & (per - 1), per);
-  ValueRow<VB> cur, nxt;
-  auto load = [&](int u, ValueRow<VB>& r) {
-    const int pos = (it.a0 + it.k0 + (u >> 2)) * kTile + 64 * ((u >> 1) & 1) + vt;
-    load_value_row<VB>(p.L, it.b, it.h, pos, it.q, u & 1, r);
+  // the thread's token inside a tile part: its code row, and its scales' places
+  const int TT = L.tile_tokens, t = vt & (TT - 1), ng = kD / L.group_v;
+  const int crow = vc_row(t, TT, L.k_bits), x = chunk_swizzle(crow, VB);
+  const int codes = L.vc_off + crow * VB * 16;
+  const bool fine = L.group_v < 64;
+  int szo[4];  // offset of the scale of 32-channel group g
+#pragma unroll
+  for (int g = 0; g < 4; ++g) szo[g] = L.vsz_off + 2 * vsz_half_index(t, 32 * g / L.group_v, TT, L.k_bits, ng, false);
+  const int zo = vsz_half_index(t, 0, TT, L.k_bits, ng, true) - vsz_half_index(t, 0, TT, L.k_bits, ng, false);
+  const int part0 = 2 * (it.a0 + it.k0) + (vt >> 6), rows = 2 * tiles;  // the thread's part of tile c: part0 + 2c
+  const int first = 128 * (it.a0 + it.k0) + vt;                        // and its position: first + 128c
+  ValueRow<VB> buf[kAhead + 1];
+  auto load = [&](int u, ValueRow<VB>& r) {  // half u % 2 of tile u / 2
+    const int c = u >> 1, half = u & 1, part = part0 + 2 * c;
+    if (u >= rows || first + 128 * c >= it.q) return;
+    const uint8_t* tp = rec.block(rec.block_of(part) + (rec.lg_part < 0 ? (vt >> 5) & 1 : 0)) + rec.tile_of(part);
+    const uint4* vc = reinterpret_cast<const uint4*>(tp + codes);
+#pragma unroll
+    for (int e = 0; e < VB / 2; ++e) {
+      const uint4 v = __ldg(vc + ((half * (VB / 2) + e) ^ x));
+      r.w[4 * e] = v.x, r.w[4 * e + 1] = v.y, r.w[4 * e + 2] = v.z, r.w[4 * e + 3] = v.w;
+    }
+    const unsigned short* sz = reinterpret_cast<const unsigned short*>(tp + (half ? szo[2] : szo[0]));
+    r.sz[0] = (uint32_t)__ldg(sz) | ((uint32_t)__ldg(sz + zo) << 16);
+    r.sz[1] = r.sz[0];
+    if (fine) {
+      sz = reinterpret_cast<const unsigned short*>(tp + (half ? szo[3] : szo[1]));
+      r.sz[1] = (uint32_t)__ldg(sz) | ((uint32_t)__ldg(sz + zo) << 16);
+    }
   };
-  load(0, nxt);
-  for (int u = 0; u < units; ++u) {
-    cur = nxt;
-    if (u + 1 < units) load(u + 1, nxt);
-    const int c = u >> 2, st = c % kVStages;
-    if ((u & 3) == 0 && c >= kVStages && !mbar_wait_warp(bar.v_empty + 8 * st, ((c / kVStages) - 1) & 1, abort)) return false;
-    const int row = 64 * ((u >> 1) & 1) + place;
-    store_value_row<VB>(cur, smem + kVOff + st * kTileBytes + (u & 1) * kHalf + row * 128, row & 7);
-    if ((u & 3) == 3) {
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) load(a, buf[a + 1]);
+#pragma unroll 1
+  for (int u = 0; u < rows; ++u) {
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) buf[a] = buf[a + 1];
+    load(u + kAhead, buf[kAhead]);
+    const int c = u >> 1, st = c % kVStages;
+    if ((u & 1) == 0 && c >= kVStages && !mbar_wait_warp(bar.v_empty + 8 * st, ((c / kVStages) - 1) & 1, abort))
+      return false;
+    const uint32_t row = smem + kVOff + st * kTileBytes + (u & 1) * kHalf + place * 128;
+    if (first + 128 * c >= it.q) {
+      zero_row(row);
+    } else {
+      uint32_t s[2], z[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        s[e] = __byte_perm(buf[0].sz[e], buf[0].sz[e], 0x1010);
+        z[e] = __byte_perm(buf[0].sz[e], buf[0].sz[e], 0x3232);
+      }
+      expand_row<VB, true>(buf[0].w, row, place & 7, [&](int pair, uint32_t& s2, uint32_t& z2) {
+        s2 = s[pair >> 4];
+        z2 = z[pair >> 4];
+      });
+    }
+    if (u & 1) {
       fence_async_smem();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive(bar.v_full + 8 * st);
@@ -552,29 +613,52 @@ __device__ bool produce_values(const ChunkParams& p, const Item& it, uint32_t sm
   }
   return true;
 }
-// Key or value tiles of phase B: rows of exact tokens, copied as they are
-// (both operands take [64-channel block][token][128 bytes]); entries past the
-// last one that a row sees are zeros.
+
+// Key or value tiles of phase B: rows of exact tokens as they are (both
+// operands take [64-channel half][token][128 bytes]). A tile of new tokens
+// only is one TMA load per half; the others (sinks, ring, the chunk's end) are
+// copied row by row, with zeros past the last token that a row sees.
 template <int STAGES>
 __device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t tiles, uint32_t full, uint32_t empty,
-                              const void* sink, const void* ring, const void* fresh, int kt, volatile int* abort) {
+                              const void* sink, const void* ring, const void* fresh, const CUtensorMap* map, int kt,
+                              volatile int* abort) {
   const LayerView& L = p.L;
   const int64_t unit = (int64_t)it.b * L.num_kv_heads + it.h;
-  const uint4* sink_p = reinterpret_cast<const uint4*>(sink) + unit * KVQ_MAX_SINKS * 16;
-  const uint4* ring_p = reinterpret_cast<const uint4*>(ring) + unit * L.residual * 16;
-  const uint4* new_p = reinterpret_cast<const uint4*>(fresh) + ((int64_t)p.in_off[it.i] * L.num_kv_heads + it.h) * 16;
-  const int held = it.s + it.n, last = held + it.t1, ch = kt & 15;
+  const int ch = kt & 15;
+  const uint4* sink_p = reinterpret_cast<const uint4*>(sink) + unit * KVQ_MAX_SINKS * 16 + ch;
+  const uint4* ring_p = reinterpret_cast<const uint4*>(ring) + unit * L.residual * 16 + ch;
+  const uint4* new_p = reinterpret_cast<const uint4*>(fresh) + ((int64_t)p.in_off[it.i] * L.num_kv_heads + it.h) * 16 + ch;
+  const int64_t stride = (int64_t)L.num_kv_heads * 16;
+  const int held = it.s + it.n, last = held + it.t1;
   const int slot0 = it.q % L.residual;  // ring slot of the first ring token
   for (int k = max(it.k0, it.nA); k < it.k1; ++k) {
     const int c = k - it.k0, st = c % STAGES, e0 = it.tile_b(k) * kTile;
     if (c >= STAGES && !mbar_wait_warp(empty + 8 * st, ((c / STAGES) - 1) & 1, abort)) return false;
-    const uint32_t dst = tiles + st * kTileBytes + (ch >> 3) * kHalf;
-#pragma unroll 8
-    for (int i = 0; i < kTile / 4; ++i) {
-      const int row = (kt >> 4) + 4 * i, e = e0 + row;
+    const uint32_t dst = tiles + st * kTileBytes, bar = full + 8 * st;
+    if (e0 >= held && e0 - held + kTile <= p.t_new[it.i]) {
+      if ((kt & 31) == 0) {
+        if (kt == 0) {
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(kTileBytes) : "memory");
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            asm volatile(
+                "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                    dst + half * kHalf),
+                "l"(map), "r"(it.h * kD + 64 * half), "r"(p.in_off[it.i] + e0 - held), "r"(bar)
+                : "memory");
+        } else {
+          mbar_arrive(bar);
+        }
+      }
+      __syncwarp();
+      continue;
+    }
+#pragma unroll 4
+    for (int i = 0; i < kTile * 16 / kProducers; ++i) {
+      const int row = (kt >> 4) + kProducers / 16 * i, e = e0 + row;
       const uint4* src;
       if (e >= held) {
-        src = new_p + (int64_t)min(e - held, it.t1) * L.num_kv_heads * 16;
+        src = new_p + min(e - held, it.t1) * stride;
       } else if (e < it.s) {
         src = sink_p + e * 16;
       } else {
@@ -582,12 +666,12 @@ __device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t til
         if (slot >= L.residual) slot -= L.residual;
         src = ring_p + slot * 16;
       }
-      cp_async16(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src + ch, e <= last);
+      cp_async16(dst + (ch >> 3) * kHalf + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src, e <= last);
     }
     asm volatile("cp.async.commit_group;\n cp.async.wait_group 0;" ::: "memory");
     fence_async_smem();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(full + 8 * st);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
   }
   return true;
 }
@@ -690,38 +774,123 @@ __device__ __forceinline__ uint32_t shuffle_bits(uint32_t x, int per) {
   }
   return x;
 }
-// Scores whose bit is clear become -inf; bits(c) gives those of columns c ..
-// c + 31.
-template <class F>
-__device__ __forceinline__ void mask_scores(uint32_t (&s)[kTile], F bits) {
-#pragma unroll
-  for (int c = 0; c < kTile; c += 32) {
-    const uint32_t m = bits(c);
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (!((m >> e) & 1u)) s[c + e] = 0xff800000u;
-  }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
-// Probabilities of one row of a tile: m (log2 units, the value subtracted) and
-// the sum l are the row's state; s becomes packed pairs written to P.
+// The state of one row's softmax, and one chunk of 32 columns (loaded in s) of
+// a tile: the maximum, a rescaling where it is due, the probabilities as packed
+// pairs over the columns 16q .. of the scores already read.
+struct RowState {
+  float m = -INFINITY;  // a whole number, or -inf
+  float l = 0.f;
+};
 template <bool BF16>
-__device__ __forceinline__ void write_probs(uint32_t (&s)[kTile], float cs, float bias, float& l, uint32_t tm_s) {
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void softmax_chunk(uint32_t (&s)[32], int q, float cs, RowState& st, uint32_t tm_s,
+                                              uint32_t tm_o, bool have_o) {
+  float mx = __uint_as_float(s[0]);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t w[16];
+  for (int c = 1; c < 31; c += 2) mx = max3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+  mx = fmaxf(mx, __uint_as_float(s[31])) * cs;
+  const bool grow = mx > st.m + kLazy;
+  if (__any_sync(0xffffffffu, grow)) {
+    const float m = grow ? ceilf(mx) : st.m;
+    const float a = grow ? ex2(st.m - m) : 1.f;  // a power of two; 0 while m = -inf
+    st.m = m;
+    st.l *= a;
+    // the slot's previous product is complete (its scores' barrier completed
+    // after it), and so O is at rest; the tile's own probabilities so far too
+    tmem_wait_st();
+    if (have_o) {
+#pragma unroll 1
+      for (int c = 0; c < kD; c += 16) {
+        uint32_t o[16];
+        tmem_ld16(tm_o + c, o);
+        tmem_wait_ld16(o);
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const float a = ex2(fmaf(__uint_as_float(s[32 * q + 2 * c]), cs, -bias));
-      const float b = ex2(fmaf(__uint_as_float(s[32 * q + 2 * c + 1]), cs, -bias));
-      sum[c & 1] += a;
-      sum[2 + (c & 1)] += b;
-      w[c] = pack2<BF16>(a, b);
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+        tmem_st16(tm_o + c, o);
+      }
     }
-    tmem_st16(tm_s + 16 * q, w);
+#pragma unroll 1
+    for (int c = 0; c < q; ++c) {
+      uint32_t w[16];
+      tmem_ld16(tm_s + 16 * c, w);
+      tmem_wait_ld16(w);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float2 f;
+        if constexpr (BF16) f = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+        else f = __half22float2(half2_of(w[e]));
+        w[e] = pack2<BF16>(f.x * a, f.y * a);
+      }
+      tmem_st16(tm_s + 16 * c, w);
+    }
   }
-  l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  const float bias = st.m == -INFINITY ? 0.f : kOffset - st.m;
+  const uint64_t cs2 = pair_of(cs, cs), b2 = pair_of(bias, bias);
+  uint64_t sum = 0;
+  uint32_t w[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    float a, b;
+    unpair(fma2(pair_of(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), cs2, b2), a, b);
+    a = ex2(a);
+    b = ex2(b);
+    sum = add2(sum, pair_of(a, b));
+    w[c] = pack2<BF16>(a, b);
+  }
+  tmem_st16(tm_s + 16 * q, w);
+  float a, b;
+  unpair(sum, a, b);
+  st.l += a + b;
+}
+// Scores whose bit is clear become -inf.
+__device__ __forceinline__ void mask_chunk(uint32_t (&s)[32], uint32_t bits) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!((bits >> e) & 1u)) s[e] = 0xff800000u;
+}
+// One tile of a row: chunks of 32 columns, the next one loading while one is
+// worked on. seen(c): bits of the columns c .. c + 31 that the row sees, where
+// some row of the item does not see all of the tile.
+template <bool BF16, class F>
+__device__ __forceinline__ void softmax_tile(float cs, RowState& st, uint32_t tm_s, uint32_t tm_o, bool have_o,
+                                             bool masked, F seen) {
+  uint32_t s[2][32];
+  tmem_ld32(tm_s, s[0]);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int q = 2 * h + e;
+      tmem_wait_ld(s[e]);
+      if (q < 3) tmem_ld32(tm_s + 32 * (q + 1), s[e ^ 1]);
+      if (masked) mask_chunk(s[e], seen(32 * q));
+      softmax_chunk<BF16>(s[e], q, cs, st, tm_s, tm_o, have_o);
+    }
+  }
 }
 
 __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32_t smem, uint32_t tmem,
@@ -735,7 +904,8 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
   const uint32_t tm_s = tmem + lanes + kTmemS + w * kTile, tm_o = tmem + lanes + kTmemO + w * kD;
   const uint32_t qtile = smem + kQOff + w * kTileBytes;
   const int n = it.slot_tiles(w);
-  float m = -INFINITY, l = 0.f, cs = 0.f;
+  RowState st;
+  float cs = 0.f;
   const int per = 32 / L.k_bits;  // key codes per word
   const int hi_b = it.s + it.n + t;                        // phase B: the row's own entry
   const int lo_b = p.window > 0 ? hi_b - p.window : -1;     // entries up to this are hidden
@@ -768,49 +938,20 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
     }
     if (!mbar_wait_warp(bar.s_full + 8 * w, j & 1, abort)) return false;
     tc_after();
-    uint32_t s[kTile];
-#pragma unroll
-    for (int c = 0; c < kTile; c += 32) tmem_ld32(tm_s + c, s + c);
-#pragma unroll
-    for (int c = 0; c < kTile; c += 32) tmem_wait_ld(s + c);
     if (in_a) {
       const int p0 = (it.a0 + k) * kTile;
-      if (p0 + kTile > it.q || p0 <= last_lo_a)
-        mask_scores(s, [&](int c) { return shuffle_bits(bit_range(lo_a + 1 - p0 - c, it.q - p0 - c), per); });
+      softmax_tile<false>(cs, st, tm_s, tm_o, j > 0, p0 + kTile > it.q || p0 <= last_lo_a, [&](int c) {
+        return shuffle_bits(bit_range(lo_a + 1 - p0 - c, it.q - p0 - c), per);
+      });
     } else {
       const int e0 = it.tile_b(k) * kTile;
-      if (e0 + kTile - 1 > first_hi || e0 <= last_lo_b)
-        mask_scores(s, [&](int c) {
-          return bit_range(lo_b + 1 - e0 - c, hi_b + 1 - e0 - c) | bit_range(0, min(it.first_e, hi_b + 1) - e0 - c);
-        });
+      const bool masked = e0 + kTile - 1 > first_hi || e0 <= last_lo_b;
+      auto seen = [&](int c) {
+        return bit_range(lo_b + 1 - e0 - c, hi_b + 1 - e0 - c) | bit_range(0, min(it.first_e, hi_b + 1) - e0 - c);
+      };
+      if (bf16) softmax_tile<true>(cs, st, tm_s, tm_o, j > 0, masked, seen);
+      else softmax_tile<false>(cs, st, tm_s, tm_o, j > 0, masked, seen);
     }
-    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-    for (int c = 0; c < kTile; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], __uint_as_float(s[c]));
-    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * cs;
-    const bool grow = mx > m + kLazy;
-    if (__any_sync(0xffffffffu, grow)) {
-      // the previous product of this slot is complete: its scores' barrier
-      // completed after it
-      const float mn = grow ? mx : m;
-      const float a = grow ? ex2(m - mn) : 1.f;  // 0 while m = -inf
-      m = mn;
-      l *= a;
-      if (j > 0) {
-#pragma unroll 1
-        for (int c = 0; c < kD; c += 16) {
-          uint32_t o[16];
-          tmem_ld16(tm_o + c, o);
-          tmem_wait_ld16(o);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-          tmem_st16(tm_o + c, o);
-        }
-      }
-    }
-    const float bias = m == -INFINITY ? 0.f : m - kOffset;
-    if (in_a || !bf16) write_probs<false>(s, cs, bias, l, tm_s);
-    else write_probs<true>(s, cs, bias, l, tm_s);
     tmem_wait_st();
     tc_before();
     __syncwarp();
@@ -834,10 +975,10 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
     float4* o = reinterpret_cast<float4*>(p.ws_o + rec * kD);
 #pragma unroll
     for (int c = 0; c < kD / 4; ++c) o[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-    p.ws_ml[rec] = make_float2(m, l);
+    p.ws_ml[rec] = make_float2(st.m, st.l);
     return true;
   }
-  const float f = 1.f / l;  // every row sees its own token
+  const float f = 1.f / st.l;  // every row sees its own token
   const int64_t at = ((int64_t)(p.in_off[it.i] + r / it.ngr) * p.num_q_heads + it.h * it.ngr + r % it.ngr) * kD;
   if (p.out_dtype == KVQ_F32) {
     float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at);
@@ -868,54 +1009,68 @@ __device__ bool issue_products(const ChunkParams& p, const Item& it, uint32_t sm
                                volatile int* abort) {
   const int steps = it.steps();
   const bool bf16 = p.L.kv_dtype == KVQ_BF16;
-  auto scores = [&](int v) -> bool {
+  // what the scores of step v need: the slot's query, the tile's keys
+  auto wait_scores = [&](int v) -> bool {
+    const int w = v & 1, c = it.both ? v >> 1 : v, k = it.k0 + c, st = c % kKStages;
+    const int j = v >> 1;
+    const bool enter_b = k >= it.nA && (j == 0 || it.slot_tile(w, j - 1) < it.nA);
+    if ((j == 0 || enter_b) && !mbar_wait(bar.q_ready + 8 * w, j == 0 ? 0 : 1, abort)) return false;
+    return (it.both && w == 1) || mbar_wait(bar.k_full + 8 * st, (c / kKStages) & 1, abort);
+  };
+  auto scores = [&](int v) {
     const int w = v & 1, c = it.both ? v >> 1 : v, k = it.k0 + c, st = c % kKStages;
     const bool in_a = k < it.nA;
-    const int j = v >> 1;
-    const bool enter_b = !in_a && (j == 0 || it.slot_tile(w, j - 1) < it.nA);
-    if (j == 0 || enter_b) {
-      if (!mbar_wait(bar.q_ready + 8 * w, j == 0 ? 0 : 1, abort)) return false;
-      tc_after();
-    }
-    if ((!it.both || w == 0) && !mbar_wait(bar.k_full + 8 * st, (c / kKStages) & 1, abort)) return false;
-    tc_after();
     const uint32_t q = smem + kQOff + w * kTileBytes, kt = smem + kKOff + st * kTileBytes;
     const uint32_t d = tmem + kTmemS + w * kTile;
     const uint32_t id = inst_desc(!in_a && bf16, in_a);
+    const uint64_t a = desc_k(q), b = in_a ? desc_mn(kt) : desc_k(kt);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint64_t a = desc_k(q + (e >> 2) * kHalf + (e & 3) * 32);
-      const uint64_t b = in_a ? desc_mn(kt + e * 2048) : desc_k(kt + (e >> 2) * kHalf + (e & 3) * 32);
-      mma_ss(d, a, b, id, e > 0);
+      const uint64_t step = ((e >> 2) * kHalf + (e & 3) * 32) >> 4;
+      mma_ss(d, a + step, b + (in_a ? (uint64_t)(e * 2048 >> 4) : step), id, e > 0);
     }
     tc_commit(bar.s_full + 8 * w);
     if (!it.both || w == 1) tc_commit(bar.k_empty + 8 * st);
-    return true;
   };
-  auto values = [&](int v) -> bool {
+  auto values = [&](int v) {
     const int w = v & 1, c = it.both ? v >> 1 : v, k = it.k0 + c, st = c % kVStages, j = v >> 1;
-    if (!mbar_wait(bar.p_ready + 8 * w, j & 1, abort)) return false;
-    if ((!it.both || w == 0) && !mbar_wait(bar.v_full + 8 * st, (c / kVStages) & 1, abort)) return false;
-    tc_after();
-    const uint32_t vt = smem + kVOff + st * kTileBytes;
     const uint32_t pa = tmem + kTmemS + w * kTile, d = tmem + kTmemO + w * kD;
     const uint32_t id = inst_desc(k >= it.nA && bf16, true);
+    const uint64_t b = desc_mn(smem + kVOff + st * kTileBytes);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) mma_ts(d, pa + 8 * e, desc_mn(vt + e * 2048), id, j > 0 || e > 0);
+    for (int e = 0; e < 8; ++e) mma_ts(d, pa + 8 * e, b + (uint64_t)(e * 2048 >> 4), id, j > 0 || e > 0);
     tc_commit(bar.pv_done + 8 * w);
     if (!it.both || w == 1) tc_commit(bar.v_empty + 8 * st);
-    return true;
   };
-  for (int v = 0; v < 2 && v < steps; ++v)
-    if (!scores(v)) return false;
+  for (int v = 0; v < 2 && v < steps; ++v) {
+    if (!wait_scores(v)) return false;
+    tc_after();
+    scores(v);
+  }
+#pragma unroll 1
   for (int v = 0; v < steps; ++v) {
-    if (!values(v)) return false;
-    if (v + 2 < steps && !scores(v + 2)) return false;
+    const int w = v & 1, c = it.both ? v >> 1 : v, st = c % kVStages;
+    // a slot that enters phase B rewrites its query only after this product
+    const bool next = v + 2 < steps;
+    const int kn = it.slot_tile(w, (v >> 1) + 1);
+    const bool enter_b = next && kn >= it.nA && it.k0 + c < it.nA;
+    if ((!it.both || w == 0) && !mbar_wait(bar.v_full + 8 * st, (c / kVStages) & 1, abort)) return false;
+    if (next && !enter_b && !wait_scores(v + 2)) return false;
+    if (!mbar_wait(bar.p_ready + 8 * w, (v >> 1) & 1, abort)) return false;
+    tc_after();
+    values(v);
+    if (next) {
+      if (enter_b) {
+        if (!wait_scores(v + 2)) return false;
+        tc_after();
+      }
+      scores(v + 2);
+    }
   }
   return true;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ ChunkMaps maps) {
   extern __shared__ uint8_t raw[];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -937,11 +1092,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKStages; ++i) {
-      mbar_init(bar.k_full + 8 * i, 2);
+      mbar_init(bar.k_full + 8 * i, kProducers / 32);
       mbar_init(bar.k_empty + 8 * i, 1);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(bar.v_full + 8 * i, 2);
+      mbar_init(bar.v_full + 8 * i, kProducers / 32);
       mbar_init(bar.v_empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -954,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -964,29 +1119,30 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
   tc_after();
   const uint32_t tmem = s_tmem;
   const Item it = find_item(p, blockIdx.x);
+  const LayerView& L = p.L;
+  const int kt = threadIdx.x & (kProducers - 1);
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     (void)softmax_slot(p, it, warp >> 2, smem, tmem, bar, abort);
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    const LayerView& L = p.L;
-    const int kt = threadIdx.x & 63;
-    if (warp < 10) {
-      const bool ok = L.k_bits == 2   ? produce_keys<2>(p, it, smem, bar, kt, abort)
-                      : L.k_bits == 4 ? produce_keys<4>(p, it, smem, bar, kt, abort)
-                                      : produce_keys<8>(p, it, smem, bar, kt, abort);
-      if (ok)
-        (void)produce_exact<kKStages>(p, it, smem + kKOff, bar.k_full, bar.k_empty, L.sink_k, L.ring_k, p.k, kt, abort);
-    } else {
-      const bool ok = L.v_bits == 2   ? produce_values<2>(p, it, smem, bar, kt, abort)
-                      : L.v_bits == 4 ? produce_values<4>(p, it, smem, bar, kt, abort)
-                                      : produce_values<8>(p, it, smem, bar, kt, abort);
-      if (ok)
-        (void)produce_exact<kVStages>(p, it, smem + kVOff, bar.v_full, bar.v_empty, L.sink_v, L.ring_v, p.v, kt, abort);
-    }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    const bool ok = L.k_bits == 2   ? produce_keys<2>(p, it, smem, bar, kt, abort)
+                    : L.k_bits == 4 ? produce_keys<4>(p, it, smem, bar, kt, abort)
+                                    : produce_keys<8>(p, it, smem, bar, kt, abort);
+    if (ok)
+      (void)produce_exact<kKStages>(p, it, smem + kKOff, bar.k_full, bar.k_empty, L.sink_k, L.ring_k, p.k, &maps.k, kt,
+                                    abort);
+  } else if (warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    const bool ok = L.v_bits == 2   ? produce_values<2>(p, it, smem, bar, kt, abort)
+                    : L.v_bits == 4 ? produce_values<4>(p, it, smem, bar, kt, abort)
+                                    : produce_values<8>(p, it, smem, bar, kt, abort);
+    if (ok)
+      (void)produce_exact<kVStages>(p, it, smem + kVOff, bar.v_full, bar.v_empty, L.sink_v, L.ring_v, p.v, &maps.v, kt,
+                                    abort);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 12 && (threadIdx.x & 31) == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == 16 && (threadIdx.x & 31) == 0) {
       if (!issue_products(p, it, smem, tmem, bar, abort)) {
         // let the products in flight finish before the tensor memory goes
         tc_commit(bar.drain);
@@ -1000,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 12)
+  if (warp == 16)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   if (threadIdx.x == 0 && s_abort) atomicOr(p.err, 1);
 }
@@ -1054,14 +1210,53 @@ __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(const
 
 }  // namespace
 
+namespace {
+
+// cuTensorMapEncodeTiled, looked up once (the runtime is the only library
+// linked).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+cudaError_t make_map(CUtensorMap& m, const ChunkParams& p, const void* data) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)p.L.num_kv_heads * kD, (cuuint64_t)p.tokens};
+  const cuuint64_t strides[1] = {(cuuint64_t)p.L.num_kv_heads * kD * 2};
+  const cuuint32_t box[2] = {64, kTile}, one[2] = {1, 1};
+  const CUtensorMapDataType t =
+      p.L.kv_dtype == KVQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUresult r = encode(&m, t, 2, const_cast<void*>(data), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
 bool chunk_tc_supported(const LayerView& L) { return L.residual_v == L.residual; }
 
 cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream) {
   if (p.items <= 0) return cudaSuccess;
-  // (set on every launch: it is per device, and a few hundred nanoseconds)
-  cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  ChunkMaps maps;
+  cudaError_t e = make_map(maps.k, p, p.k);
+  if (e == cudaSuccess) e = make_map(maps.v, p, p.v);
   if (e != cudaSuccess) return e;
-  chunk_tc_kernel<<<p.items, kThreads, kSmemBytes, stream>>>(p);
+  // (set on every launch: it is per device, and a few hundred nanoseconds)
+  e = cudaFuncSetAttribute(chunk_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  chunk_tc_kernel<<<p.items, kThreads, kSmemBytes, stream>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.merge_rows == 0) return e;
   chunk_combine_kernel<<<(unsigned)((p.merge_rows + kCombineWarps - 1) / kCombineWarps), 32 * kCombineWarps, 0, stream>>>(p);
