@@ -19,8 +19,9 @@
 // parts are merged by chunk_combine_kernel.
 //
 // Warps: 0-3 and 4-7 the softmax of slots 0 and 1 (a thread owns a row, so
-// maxima, sums and the rotation of a row need no exchange), 8-11 key tiles,
-// 12-15 value tiles, 16 issues the MMAs (17-19 idle: registers move between
+// maxima, sums and the rotation of a row need no exchange), 8, 9, 12, 13 key
+// tiles, 10, 11, 14, 15 value tiles (each kind on two of the four schedulers),
+// 16 issues the MMAs (17-19 idle: registers move between
 // whole warpgroups, setmaxnreg 144 + 144 + 72 + 72 + 48 = 5 x 96). The hot
 // loops are kept short (32 columns, one row of codes at a time): four roles
 // share an SM's instruction caches, and unrolled whole tiles spent most of
@@ -36,10 +37,11 @@
 // Queries are scaled by a power of two per row (exact but for
 // subnormals), so that any bf16 query fits fp16. Phase B: keys, values,
 // queries and probabilities in the kv dtype, keys K-major.
-// Softmax: probabilities are 2^(z - m + 8) with m a whole number that is raised
-// only when a row's maximum passes it by more than 4 (log2 units): one pass over the
-// scores, rescaling of O and of what the tile has written rare and exact (powers of two), and fp16
-// probabilities keep 14 + 8 binary orders below m before they turn subnormal.
+// Softmax: probabilities are 2^(z - m + 6) with m a whole number that is raised
+// only when a row's maximum passes it by more than 8 (log2 units): one pass over
+// the scores; rescaling O and what the tile has written is rare and exact (powers
+// of two); fp16 probabilities reach 2^14 and keep 14 + 6 binary orders below m
+// before they turn subnormal.
 //
 // Every wait is bounded (~2 s): a thread that gives up sets the device error
 // word and an abort flag that ends the others' waits.
@@ -63,7 +65,7 @@ constexpr int kQOff = 0, kKOff = 2 * kTileBytes, kVOff = kKOff + kKStages * kTil
 constexpr int kBarOff = kVOff + kVStages * kTileBytes;
 constexpr int kSmemBytes = kBarOff + 256 + 1024;  // + alignment of the base to 1024
 constexpr int kTmemS = 0, kTmemO = 256;           // columns of slot 0; slot 1 is 128 further
-constexpr float kLazy = 4.f, kOffset = 8.f;
+constexpr float kLazy = 8.f, kOffset = 6.f;
 constexpr long long kWaitCycles = 4000000000LL;
 
 // ------------------------------------------------------------- PTX helpers
@@ -357,34 +359,50 @@ __device__ __forceinline__ void zero_row(uint32_t row) {
   for (int c = 0; c < 8; ++c) sts16(row + (c << 4), 0u, 0u, 0u, 0u);
 }
 
-// A block record by its index, and by the index of its 64-token part (with
-// 32-token blocks: the part's first block).
-struct Records {
-  const uint8_t* base;   // contiguous: the unit's first record; paged: the pool
-  const int32_t* table;  // paged: the sequence's row of the page table
-  int64_t bytes;
-  uint32_t per_page, hkv, h;
-  int lg_part;  // log2(64-token parts per block); -1: two blocks per part
-  int tile0, tile_bytes;
-  __device__ __forceinline__ Records(const LayerView& L, int b, int h_) {
-    table = L.page_table ? L.page_table + (int64_t)b * L.max_pages : nullptr;
-    bytes = L.record_bytes;
-    per_page = (uint32_t)L.page_blocks;
-    hkv = (uint32_t)L.num_kv_heads;
-    h = (uint32_t)h_;
-    base = table ? L.blocks : L.blocks + ((int64_t)b * L.num_kv_heads + h_) * L.max_blocks * bytes;
-    lg_part = L.group_k == 128 ? 1 : L.group_k == 64 ? 0 : -1;
-    tile0 = L.tile0_off;
-    tile_bytes = L.tile_bytes;
-  }
-  __device__ __forceinline__ const uint8_t* block(uint32_t j) const {
-    if (!table) return base + j * bytes;
+// Walks one 64-token part of every tile of a unit (part 0 or 1 of tiles a0,
+// a0 + 1, ...): the address of its tile inside its block record. A step is one
+// addition, but where a page of a paged cache ends.
+struct PartCursor {
+  const uint8_t* at;     // the part's tile (32-token blocks: its first block)
+  const uint8_t* base;   // contiguous: the unit's first record; paged: the pool at the unit's head
+  const int32_t* table;  // paged: the sequence's row of the page table, else null
+  int64_t step;          // bytes from one tile's part to the next one's
+  uint32_t block, in_page, per_page, blocks, end;  // current block, ...; blocks per step; blocks of the sequence
+  int offset;            // of the part's tile in its record
+  __device__ __forceinline__ const uint8_t* find(uint32_t j, const LayerView& L) const {
+    if (!table) return base + (int64_t)j * L.record_bytes;
     const uint32_t run = j / per_page;
-    return base + (((int64_t)__ldg(table + run) * hkv + h) * per_page + (j - run * per_page)) * bytes;
+    return base + ((int64_t)__ldg(table + run) * L.num_kv_heads * per_page + (j - run * per_page)) * L.record_bytes;
   }
-  __device__ __forceinline__ int block_of(int part) const { return lg_part < 0 ? 2 * part : part >> lg_part; }
-  // byte offset of a part's tile in its record
-  __device__ __forceinline__ int tile_of(int part) const { return tile0 + (lg_part == 1 ? (part & 1) * tile_bytes : 0); }
+  __device__ __forceinline__ void init(const LayerView& L, int b, int h, int q, int part) {
+    const bool paged = L.page_table != nullptr;
+    table = paged ? L.page_table + (int64_t)b * L.max_pages : nullptr;
+    per_page = paged ? (uint32_t)L.page_blocks : 0xffffffffu;
+    base = L.blocks + (paged ? (int64_t)h * L.page_blocks : ((int64_t)b * L.num_kv_heads + h) * L.max_blocks) *
+                          L.record_bytes;
+    const int G = L.group_k;
+    offset = L.tile0_off + (G == 128 ? (part & 1) * L.tile_bytes : 0);
+    blocks = (uint32_t)(kTile / G);
+    step = (int64_t)blocks * L.record_bytes;
+    end = (uint32_t)(q / G);
+    block = (uint32_t)(part * 64 / G);
+    in_page = paged ? block % per_page : 0u;
+    at = block < end ? find(block, L) + offset : base;
+  }
+  __device__ __forceinline__ void next(const LayerView& L) {
+    block += blocks;
+    in_page += blocks;
+    if (in_page >= per_page) {  // never in a contiguous cache (fewer than 2^30 blocks)
+      in_page = block % per_page;
+      if (block < end) at = find(block, L) + offset;
+    } else {
+      at += step;
+    }
+  }
+  // 32-token blocks: the part's second block
+  __device__ __forceinline__ const uint8_t* second(const LayerView& L) const {
+    return in_page + 1 < per_page ? at + L.record_bytes : find(block + 1, L) + offset;
+  }
 };
 
 // 64 key codes of one channel in token order, with the scales of their one or
@@ -408,33 +426,35 @@ __device__ __forceinline__ KeyChannel key_channel(const LayerView& L, int d) {
   c.sz = (L.rec_ksz_off >= 0 ? L.rec_ksz_off - L.tile0_off : L.ksz_off) + 4 * d;
   return c;
 }
-// Loads a row of part `part`; `valid` tokens of it exist (0, 32 or 64).
+// Loads the channel's row of the cursor's part; `valid` tokens of it exist
+// (<= 0, 32 or >= 64).
 template <int KB>
-__device__ __forceinline__ void load_key_row(const Records& rec, int part, int valid, const KeyChannel& c, bool axis0,
-                                             KeyRow<KB>& r) {
+__device__ __forceinline__ void load_key_row(const LayerView& L, const PartCursor& cur, int valid, const KeyChannel& c,
+                                             bool wide, bool axis0, KeyRow<KB>& r) {
   if (valid <= 0) return;
-  if (rec.lg_part >= 0) {
-    const uint8_t* record = rec.block(rec.block_of(part));
-    const uint8_t* tp = record + rec.tile_of(part);
-    const uint4* kc = reinterpret_cast<const uint4*>(tp + c.codes);
+  const uint8_t* tp = cur.at;
+  if (wide) {
+    const uint8_t* kc = tp + c.codes;
 #pragma unroll
     for (int e = 0; e < KB / 2; ++e) {
-      const uint4 v = __ldg(kc + (e ^ c.x));
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(kc + ((e ^ c.x) << 4)));
       r.w[4 * e] = v.x, r.w[4 * e + 1] = v.y, r.w[4 * e + 2] = v.z, r.w[4 * e + 3] = v.w;
     }
-    // (a record's shared scales sit at a fixed place before its first tile)
-    if (axis0) r.sz[0] = __ldg(reinterpret_cast<const uint32_t*>((rec.lg_part == 1 ? record + rec.tile0 : tp) + c.sz));
+    // (128-token blocks keep a channel's scales once, before the first tile)
+    if (axis0) r.sz[0] = __ldg(reinterpret_cast<const uint32_t*>(tp + (L.rec_ksz_off >= 0 ? L.tile0_off - cur.offset : 0) + c.sz));
     r.sz[1] = r.sz[0];
   } else {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      if (e == 1 && valid <= 32) {
+      if (e == 1) {
+        if (valid <= 32) {
 #pragma unroll
-        for (int i = 0; i < KB; ++i) r.w[KB + i] = 0u;
-        r.sz[1] = 0u;
-        break;
+          for (int i = 0; i < KB; ++i) r.w[KB + i] = 0u;
+          r.sz[1] = 0u;
+          break;
+        }
+        tp = cur.second(L);
       }
-      const uint8_t* tp = rec.block(rec.block_of(part) + e);
       if constexpr (KB == 2) {
         const uint2 v = __ldg(reinterpret_cast<const uint2*>(tp + c.codes));
         r.w[2 * e] = v.x, r.w[2 * e + 1] = v.y;
@@ -484,49 +504,60 @@ struct Bars {
   uint32_t k_full, k_empty, v_full, v_empty, s_full, p_ready, pv_done, q_ready, drain;  // addresses of arrays of barriers
 };
 
-// Key tiles of phase A: thread kt expands channel kt of both 64-token parts of
-// a tile. A row's codes are loaded kAhead rows before they are expanded.
+// Key tiles of phase A: thread kt expands channels kt % 64 and kt % 64 + 64 of
+// the 64-token part kt / 64 of a tile, one row after the other; a row is loaded
+// while the one before it is expanded.
 template <int KB>
 __device__ bool produce_keys(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, int kt,
                              volatile int* abort) {
   const int tiles = min(it.k1, it.nA) - it.k0;
   if (tiles <= 0) return true;
-  constexpr int kAhead = KB == 8 ? 1 : 2;
-  const Records rec(p.L, it.b, it.h);
-  const bool axis0 = p.L.k_axis == 0;
-  const KeyChannel ch = key_channel<KB>(p.L, kt);
-  const int part0 = 2 * (it.a0 + it.k0), rows = 2 * tiles;
-  KeyRow<KB> buf[kAhead + 1];
-  auto load = [&](int u, KeyRow<KB>& r) {
-    load_key_row<KB>(rec, part0 + u, u < rows ? it.q - 64 * (part0 + u) : 0, ch, axis0, r);
-  };
-#pragma unroll
-  for (int a = 0; a < kAhead; ++a) load(a, buf[a + 1]);
+  const LayerView& L = p.L;
+  const bool axis0 = L.k_axis == 0, wide = L.group_k >= 64;
+  const int part = kt >> 6, d0 = kt & 63;
+  const KeyChannel ch = key_channel<KB>(L, d0);
+  const int up = key_channel<KB>(L, 64).codes - key_channel<KB>(L, 0).codes;  // to channel d + 64 (same swizzle)
+  PartCursor cur;
+  cur.init(L, it.b, it.h, it.q, 2 * (it.a0 + it.k0) + part);
+  int valid = it.q - (it.a0 + it.k0) * kTile - 64 * part;  // positions of the part that exist, and of those after it
+  KeyRow<KB> row, next;
+  load_key_row<KB>(L, cur, valid, ch, wide, axis0, next);
+  const int stride = 4 * (kD / L.group_v);
+  const uint32_t dst = smem + kKOff + part * kHalf + d0 * 128;
+  int st = 0;
+  uint32_t phase = 1;  // of the stage's empty barrier: the first pass does not wait
 #pragma unroll 1
-  for (int u = 0; u < rows; ++u) {
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) buf[a] = buf[a + 1];
-    load(u + kAhead, buf[kAhead]);
-    const int c = u >> 1, st = c % kKStages, part = part0 + u, valid = it.q - 64 * part;
-    if ((u & 1) == 0 && c >= kKStages && !mbar_wait_warp(bar.k_empty + 8 * st, ((c / kKStages) - 1) & 1, abort))
-      return false;
-    const uint32_t row = smem + kKOff + st * kTileBytes + (u & 1) * kHalf + kt * 128;
-    if (valid <= 0) {
-      zero_row(row);
-    } else if (axis0) {
-      store_key_row<KB>(buf[0], row, kt);
-    } else {
-      const int stride = 4 * (kD / p.L.group_v), at = p.L.ksz_off + 4 * (kt / p.L.group_v);
-      const uint8_t* tok = rec.block(rec.block_of(part)) + rec.tile_of(part) + at;
-      const uint8_t* tok2 = rec.lg_part >= 0 ? tok + 32 * stride
-                            : valid > 32     ? rec.block(rec.block_of(part) + 1) + at
-                                             : tok;
-      store_key_row_per_token<KB>(buf[0], row, kt, tok, tok2, stride);
+  for (int u = 0; u < 2 * tiles; ++u) {
+    const int e = u & 1;  // channel d0 + 64 e
+    row = next;
+    const int here = valid;
+    const uint8_t *tok = cur.at, *tok2 = cur.at;
+    if (!axis0 && here > 0) {
+      const int at = L.ksz_off + 4 * ((d0 + 64 * e) / L.group_v);
+      tok = cur.at + at;
+      tok2 = wide ? tok + 32 * stride : here > 32 ? cur.second(L) + at : tok;
     }
-    if (u & 1) {
+    if (e) {
+      cur.next(L);
+      valid -= kTile;
+    }
+    KeyChannel c = ch;
+    c.codes += e ? 0 : up;
+    c.sz += e ? 0 : 256;
+    load_key_row<KB>(L, cur, u + 1 < 2 * tiles ? valid : 0, c, wide, axis0, next);
+    if (!e && !mbar_wait_warp(bar.k_empty + 8 * st, phase, abort)) return false;
+    const uint32_t at = dst + st * kTileBytes + e * (64 * 128);
+    if (here <= 0) zero_row(at);
+    else if (axis0) store_key_row<KB>(row, at, d0);
+    else store_key_row_per_token<KB>(row, at, d0, tok, tok2, stride);
+    if (e) {
       fence_async_smem();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive(bar.k_full + 8 * st);
+      if (++st == kKStages) {
+        st = 0;
+        phase ^= 1u;
+      }
     }
   }
   return true;
@@ -538,77 +569,90 @@ struct ValueRow {
   uint32_t w[2 * VB];
   uint32_t sz[2];  // (scale, zero) of the first and second 32 channels
 };
-// Value tiles of phase A: thread vt expands token vt of a tile, both 64-channel
-// halves, into the keys' token order. Loads as for the keys.
+// Value tiles of phase A: thread vt expands token vt of a tile, one 64-channel
+// half after the other, into the keys' token order; loads as for the keys.
 template <int VB>
 __device__ bool produce_values(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, int vt,
                                volatile int* abort) {
   const int tiles = min(it.k1, it.nA) - it.k0;
   if (tiles <= 0) return true;
-  constexpr int kAhead = VB == 8 ? 1 : 2;
   const LayerView& L = p.L;
-  const Records rec(L, it.b, it.h);
   const int per = 32 / L.k_bits;
   const int place = (vt & ~(per - 1)) + place_of(vt & (per - 1), per);
   // the thread's token inside a tile part: its code row, and its scales' places
   const int TT = L.tile_tokens, t = vt & (TT - 1), ng = kD / L.group_v;
   const int crow = vc_row(t, TT, L.k_bits), x = chunk_swizzle(crow, VB);
   const int codes = L.vc_off + crow * VB * 16;
-  const bool fine = L.group_v < 64;
-  int szo[4];  // offset of the scale of 32-channel group g
-#pragma unroll
-  for (int g = 0; g < 4; ++g) szo[g] = L.vsz_off + 2 * vsz_half_index(t, 32 * g / L.group_v, TT, L.k_bits, ng, false);
+  const bool fine = L.group_v < 64, second = TT == 32 && (vt & 32);
+  auto scale_at = [&](int g) {  // offset of the scale of 32-channel group g
+    return L.vsz_off + 2 * vsz_half_index(t, 32 * g / L.group_v, TT, L.k_bits, ng, false);
+  };
+  const int sz0 = scale_at(0), sz2 = scale_at(2), fine_step = scale_at(1) - sz0;  // (groups are evenly spaced)
   const int zo = vsz_half_index(t, 0, TT, L.k_bits, ng, true) - vsz_half_index(t, 0, TT, L.k_bits, ng, false);
-  const int part0 = 2 * (it.a0 + it.k0) + (vt >> 6), rows = 2 * tiles;  // the thread's part of tile c: part0 + 2c
-  const int first = 128 * (it.a0 + it.k0) + vt;                        // and its position: first + 128c
-  ValueRow<VB> buf[kAhead + 1];
-  auto load = [&](int u, ValueRow<VB>& r) {  // half u % 2 of tile u / 2
-    const int c = u >> 1, half = u & 1, part = part0 + 2 * c;
-    if (u >= rows || first + 128 * c >= it.q) return;
-    const uint8_t* tp = rec.block(rec.block_of(part) + (rec.lg_part < 0 ? (vt >> 5) & 1 : 0)) + rec.tile_of(part);
-    const uint4* vc = reinterpret_cast<const uint4*>(tp + codes);
+  PartCursor cur;
+  cur.init(L, it.b, it.h, it.q, 2 * (it.a0 + it.k0) + (vt >> 6));
+  int valid = it.q - (it.a0 + it.k0) * kTile - vt;  // > 0: the thread's token exists
+  const uint8_t* tp = nullptr;                      // its tile
+  ValueRow<VB> row, next;
+  auto load = [&](int half) {
+    const uint8_t* vc = tp + codes;
 #pragma unroll
     for (int e = 0; e < VB / 2; ++e) {
-      const uint4 v = __ldg(vc + ((half * (VB / 2) + e) ^ x));
-      r.w[4 * e] = v.x, r.w[4 * e + 1] = v.y, r.w[4 * e + 2] = v.z, r.w[4 * e + 3] = v.w;
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(vc + (((half * (VB / 2) + e) ^ x) << 4)));
+      next.w[4 * e] = v.x, next.w[4 * e + 1] = v.y, next.w[4 * e + 2] = v.z, next.w[4 * e + 3] = v.w;
     }
-    const unsigned short* sz = reinterpret_cast<const unsigned short*>(tp + (half ? szo[2] : szo[0]));
-    r.sz[0] = (uint32_t)__ldg(sz) | ((uint32_t)__ldg(sz + zo) << 16);
-    r.sz[1] = r.sz[0];
+    const unsigned short* sz = reinterpret_cast<const unsigned short*>(tp + (half ? sz2 : sz0));
+    next.sz[0] = (uint32_t)__ldg(sz) | ((uint32_t)__ldg(sz + zo) << 16);
+    next.sz[1] = next.sz[0];
     if (fine) {
-      sz = reinterpret_cast<const unsigned short*>(tp + (half ? szo[3] : szo[1]));
-      r.sz[1] = (uint32_t)__ldg(sz) | ((uint32_t)__ldg(sz + zo) << 16);
+      sz += fine_step / 2;
+      next.sz[1] = (uint32_t)__ldg(sz) | ((uint32_t)__ldg(sz + zo) << 16);
     }
   };
-#pragma unroll
-  for (int a = 0; a < kAhead; ++a) load(a, buf[a + 1]);
+  if (valid > 0) {
+    tp = second ? cur.second(L) : cur.at;
+    load(0);
+  }
+  const uint32_t dst = smem + kVOff + place * 128;
+  int st = 0;
+  uint32_t phase = 1;
 #pragma unroll 1
-  for (int u = 0; u < rows; ++u) {
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) buf[a] = buf[a + 1];
-    load(u + kAhead, buf[kAhead]);
-    const int c = u >> 1, st = c % kVStages;
-    if ((u & 1) == 0 && c >= kVStages && !mbar_wait_warp(bar.v_empty + 8 * st, ((c / kVStages) - 1) & 1, abort))
-      return false;
-    const uint32_t row = smem + kVOff + st * kTileBytes + (u & 1) * kHalf + place * 128;
-    if (first + 128 * c >= it.q) {
-      zero_row(row);
+  for (int u = 0; u < 2 * tiles; ++u) {
+    const int e = u & 1;
+    row = next;
+    const bool here = valid > 0;
+    if (e) {
+      cur.next(L);
+      valid -= kTile;
+    }
+    if (u + 1 < 2 * tiles && valid > 0) {
+      if (e) tp = second ? cur.second(L) : cur.at;
+      load(e ^ 1);
+    }
+    if (!e && !mbar_wait_warp(bar.v_empty + 8 * st, phase, abort)) return false;
+    const uint32_t at = dst + st * kTileBytes + e * kHalf;
+    if (!here) {
+      zero_row(at);
     } else {
       uint32_t s[2], z[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s[e] = __byte_perm(buf[0].sz[e], buf[0].sz[e], 0x1010);
-        z[e] = __byte_perm(buf[0].sz[e], buf[0].sz[e], 0x3232);
+      for (int i = 0; i < 2; ++i) {
+        s[i] = __byte_perm(row.sz[i], row.sz[i], 0x1010);
+        z[i] = __byte_perm(row.sz[i], row.sz[i], 0x3232);
       }
-      expand_row<VB, true>(buf[0].w, row, place & 7, [&](int pair, uint32_t& s2, uint32_t& z2) {
+      expand_row<VB, true>(row.w, at, place & 7, [&](int pair, uint32_t& s2, uint32_t& z2) {
         s2 = s[pair >> 4];
         z2 = z[pair >> 4];
       });
     }
-    if (u & 1) {
+    if (e) {
       fence_async_smem();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive(bar.v_full + 8 * st);
+      if (++st == kVStages) {
+        st = 0;
+        phase ^= 1u;
+      }
     }
   }
   return true;
@@ -873,11 +917,11 @@ __device__ __forceinline__ void mask_chunk(uint32_t (&s)[32], uint32_t bits) {
     if (!((bits >> e) & 1u)) s[e] = 0xff800000u;
 }
 // One tile of a row: chunks of 32 columns, the next one loading while one is
-// worked on. seen(c): bits of the columns c .. c + 31 that the row sees, where
-// some row of the item does not see all of the tile.
-template <bool BF16, class F>
+// worked on. MASKED (some row of the item does not see all of the tile; apart
+// from the common loop): seen(c) gives the columns c .. c + 31 that the row sees.
+template <bool BF16, bool MASKED, class F>
 __device__ __forceinline__ void softmax_tile(float cs, RowState& st, uint32_t tm_s, uint32_t tm_o, bool have_o,
-                                             bool masked, F seen) {
+                                             F seen) {
   uint32_t s[2][32];
   tmem_ld32(tm_s, s[0]);
 #pragma unroll 1
@@ -887,7 +931,7 @@ __device__ __forceinline__ void softmax_tile(float cs, RowState& st, uint32_t tm
       const int q = 2 * h + e;
       tmem_wait_ld(s[e]);
       if (q < 3) tmem_ld32(tm_s + 32 * (q + 1), s[e ^ 1]);
-      if (masked) mask_chunk(s[e], seen(32 * q));
+      if constexpr (MASKED) mask_chunk(s[e], seen(32 * q));
       softmax_chunk<BF16>(s[e], q, cs, st, tm_s, tm_o, have_o);
     }
   }
@@ -938,19 +982,19 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
     }
     if (!mbar_wait_warp(bar.s_full + 8 * w, j & 1, abort)) return false;
     tc_after();
-    if (in_a) {
-      const int p0 = (it.a0 + k) * kTile;
-      softmax_tile<false>(cs, st, tm_s, tm_o, j > 0, p0 + kTile > it.q || p0 <= last_lo_a, [&](int c) {
-        return shuffle_bits(bit_range(lo_a + 1 - p0 - c, it.q - p0 - c), per);
-      });
-    } else {
-      const int e0 = it.tile_b(k) * kTile;
-      const bool masked = e0 + kTile - 1 > first_hi || e0 <= last_lo_b;
+    const int at = in_a ? (it.a0 + k) * kTile : it.tile_b(k) * kTile;  // the tile's first position or entry
+    const bool masked = in_a ? at + kTile > it.q || at <= last_lo_a : at + kTile - 1 > first_hi || at <= last_lo_b;
+    if (masked) {
       auto seen = [&](int c) {
-        return bit_range(lo_b + 1 - e0 - c, hi_b + 1 - e0 - c) | bit_range(0, min(it.first_e, hi_b + 1) - e0 - c);
+        if (in_a) return shuffle_bits(bit_range(lo_a + 1 - at - c, it.q - at - c), per);
+        return bit_range(lo_b + 1 - at - c, hi_b + 1 - at - c) | bit_range(0, min(it.first_e, hi_b + 1) - at - c);
       };
-      if (bf16) softmax_tile<true>(cs, st, tm_s, tm_o, j > 0, masked, seen);
-      else softmax_tile<false>(cs, st, tm_s, tm_o, j > 0, masked, seen);
+      if (in_a || !bf16) softmax_tile<false, true>(cs, st, tm_s, tm_o, j > 0, seen);
+      else softmax_tile<true, true>(cs, st, tm_s, tm_o, j > 0, seen);
+    } else {
+      auto all = [](int) { return 0xffffffffu; };
+      if (in_a || !bf16) softmax_tile<false, false>(cs, st, tm_s, tm_o, j > 0, all);
+      else softmax_tile<true, false>(cs, st, tm_s, tm_o, j > 0, all);
     }
     tmem_wait_st();
     tc_before();
@@ -1120,11 +1164,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
   const uint32_t tmem = s_tmem;
   const Item it = find_item(p, blockIdx.x);
   const LayerView& L = p.L;
-  const int kt = threadIdx.x & (kProducers - 1);
+  const int kt = ((warp >> 2) & 1) * 64 + (threadIdx.x & 63);  // of 128 key or value threads
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     (void)softmax_slot(p, it, warp >> 2, smem, tmem, bar, abort);
-  } else if (warp < 12) {
+  } else if (warp < 16 && !(warp & 2)) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const bool ok = L.k_bits == 2   ? produce_keys<2>(p, it, smem, bar, kt, abort)
                     : L.k_bits == 4 ? produce_keys<4>(p, it, smem, bar, kt, abort)
