@@ -21,7 +21,7 @@
 // Warps: 0-3 and 4-7 the softmax of slots 0 and 1 (a thread owns a row, so
 // maxima, sums and the rotation of a row need no exchange), 8, 9, 12, 13 key
 // tiles, 10, 11, 14, 15 value tiles (each kind on two of the four schedulers),
-// 16 issues the MMAs (17-19 idle: registers move between
+// 16 issues the MMAs, 17 copies packed parts (18, 19 idle: registers move between
 // whole warpgroups, setmaxnreg 144 + 144 + 72 + 72 + 48 = 5 x 96). The hot
 // loops are kept short (32 columns, one row of codes at a time): four roles
 // share an SM's instruction caches, and unrolled whole tiles spent most of
@@ -58,12 +58,15 @@ namespace {
 constexpr int kRows = kChunkSlotRows, kTile = kChunkTile, kD = kHeadDim;
 constexpr int kThreads = 640;
 constexpr int kProducers = 128;  // threads of the key warps, and of the value warps
-constexpr int kKStages = 2, kVStages = 3;
+constexpr int kKStages = 2, kVStages = 2;
+constexpr int kRawStages = 4;           // raw stages at most
 constexpr int kTileBytes = kTile * kD * 2;
 constexpr int kHalf = kTileBytes / 2;  // one 64-wide block of a tile: 128 rows of 128 bytes
 constexpr int kQOff = 0, kKOff = 2 * kTileBytes, kVOff = kKOff + kKStages * kTileBytes;
 constexpr int kBarOff = kVOff + kVStages * kTileBytes;
-constexpr int kSmemBytes = kBarOff + 256 + 1024;  // + alignment of the base to 1024
+constexpr int kRawOff = kBarOff + 256, kRawBytes = 34304;  // packed parts: at most 18,432 bytes each
+constexpr int kSmemBytes = kRawOff + kRawBytes + 1024;     // + alignment of the base to 1024
+static_assert(kSmemBytes + 128 <= 227 * 1024, "shared memory of one CTA");
 constexpr int kTmemS = 0, kTmemO = 256;           // columns of slot 0; slot 1 is 128 further
 constexpr float kLazy = 8.f, kOffset = 6.f;
 constexpr long long kWaitCycles = 4000000000LL;
@@ -99,7 +102,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
   return true;
 }
-// The same by a whole warp: all lanes go on, or none.
+// After an abort: waits for copies or products in flight (or ~2 s).
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try(bar, parity) && clock64() - t0 < kWaitCycles) {
+  }
+}
+// mbar_wait by a whole warp: all lanes go on, or none.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
@@ -318,8 +327,8 @@ __host__ __device__ inline int place_of(int j, int per) {
 __host__ __device__ inline int code_at(int c, int per) { return per == 4 ? c : ((c & 1) ? per / 2 : 0) + (c >> 1); }
 
 // Expands 64 codes (2 * B words) into a 128-byte row of fp16 at `row`, chunk
-// c at c ^ x. sz(place) gives the (scale, zero point) half2 pairs of the two
-// codes at places 2i, 2i + 1: {(s, s), (z, z)}.
+// c at c ^ x. sz(word, pair, s2, z2) gives the (scale, scale) and (zero, zero)
+// halves of the two codes of a pair.
 // NATURAL: the codes' own order instead, one more permute per pair.
 template <int B, bool NATURAL, class SZ>
 __device__ __forceinline__ void expand_row(const uint32_t (&w)[2 * B], uint32_t row, int x, SZ sz) {
@@ -331,7 +340,7 @@ __device__ __forceinline__ void expand_row(const uint32_t (&w)[2 * B], uint32_t 
 #pragma unroll
     for (int i = 0; i < pairs; ++i) {
       uint32_t s2, z2;
-      sz(j * pairs + i, s2, z2);
+      sz(j, j * pairs + i, s2, z2);
       h[i] = bits2(__hfma2(code_pair<B>(w[j], w8, i), half2_of(s2), half2_of(z2)));
     }
     if constexpr (NATURAL && B != 8) {
@@ -359,198 +368,193 @@ __device__ __forceinline__ void zero_row(uint32_t row) {
   for (int c = 0; c < 8; ++c) sts16(row + (c << 4), 0u, 0u, 0u, 0u);
 }
 
-// Walks one 64-token part of every tile of a unit (part 0 or 1 of tiles a0,
-// a0 + 1, ...): the address of its tile inside its block record. A step is one
-// addition, but where a page of a paged cache ends.
-struct PartCursor {
-  const uint8_t* at;     // the part's tile (32-token blocks: its first block)
-  const uint8_t* base;   // contiguous: the unit's first record; paged: the pool at the unit's head
-  const int32_t* table;  // paged: the sequence's row of the page table, else null
-  int64_t step;          // bytes from one tile's part to the next one's
-  uint32_t block, in_page, per_page, blocks, end;  // current block, ...; blocks per step; blocks of the sequence
-  int offset;            // of the part's tile in its record
-  __device__ __forceinline__ const uint8_t* find(uint32_t j, const LayerView& L) const {
-    if (!table) return base + (int64_t)j * L.record_bytes;
-    const uint32_t run = j / per_page;
-    return base + ((int64_t)__ldg(table + run) * L.num_kv_heads * per_page + (j - run * per_page)) * L.record_bytes;
+struct Bars {  // shared-memory addresses of arrays of barriers
+  uint32_t k_full, k_empty, v_full, v_empty, s_full, p_ready, pv_done, q_ready, raw_full, raw_empty, drain;
+};
+
+// Packed parts. Warp 17 copies every 64-token part of the item's quantized
+// tiles (one block, a tile of a 128-token block with the block's key scales, or
+// two 32-token blocks) into a ring of raw stages; the key and value warps
+// expand from there. What a producer thread reads of a part sits at offsets
+// that it works out once.
+struct RawLayout {
+  int bytes, stages;  // of a stage
+  int tile;           // offset of the (first) tile in a stage: 512 with shared key scales, else 0
+  __device__ __forceinline__ explicit RawLayout(const LayerView& L) {
+    tile = L.rec_ksz_off >= 0 ? kD * 4 : 0;
+    bytes = L.group_k == 32 ? 2 * (int)L.record_bytes : tile + L.tile_bytes;
+    bytes = (bytes + 127) & ~127;
+    stages = min(kRawStages, kRawBytes / bytes);
   }
-  __device__ __forceinline__ void init(const LayerView& L, int b, int h, int q, int part) {
-    const bool paged = L.page_table != nullptr;
-    table = paged ? L.page_table + (int64_t)b * L.max_pages : nullptr;
-    per_page = paged ? (uint32_t)L.page_blocks : 0xffffffffu;
-    base = L.blocks + (paged ? (int64_t)h * L.page_blocks : ((int64_t)b * L.num_kv_heads + h) * L.max_blocks) *
-                          L.record_bytes;
-    const int G = L.group_k;
-    offset = L.tile0_off + (G == 128 ? (part & 1) * L.tile_bytes : 0);
-    blocks = (uint32_t)(kTile / G);
-    step = (int64_t)blocks * L.record_bytes;
-    end = (uint32_t)(q / G);
-    block = (uint32_t)(part * 64 / G);
-    in_page = paged ? block % per_page : 0u;
-    at = block < end ? find(block, L) + offset : base;
+};
+// A walk over the ring: stage and the parity of its next phase.
+struct RawRing {
+  int stage = 0, stages;
+  uint32_t parity = 0;
+  __device__ __forceinline__ explicit RawRing(int n) : stages(n) {}
+  __device__ __forceinline__ void next() {
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1u;
+    }
   }
-  __device__ __forceinline__ void next(const LayerView& L) {
-    block += blocks;
-    in_page += blocks;
-    if (in_page >= per_page) {  // never in a contiguous cache (fewer than 2^30 blocks)
-      in_page = block % per_page;
-      if (block < end) at = find(block, L) + offset;
+};
+__device__ __forceinline__ void bulk_g2s(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+// One thread.
+__device__ bool copy_parts(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, volatile int* abort) {
+  const LayerView& L = p.L;
+  const int tiles = min(it.k1, it.nA) - it.k0;
+  const RawLayout raw(L);
+  RawRing ring(raw.stages);
+  const int G = L.group_k;
+  for (int u = 0; u < 2 * tiles; ++u, ring.next()) {
+    const int pos = (it.a0 + it.k0) * kTile + 64 * u;
+    if (u >= raw.stages && !mbar_wait(bar.raw_empty + 8 * ring.stage, ring.parity ^ 1u, abort)) {
+      for (int v = u - raw.stages; v < u; ++v) mbar_drain(bar.raw_full + 8 * (v % raw.stages), (v / raw.stages) & 1);
+      return false;
+    }
+    const uint32_t full = bar.raw_full + 8 * ring.stage, dst = smem + kRawOff + ring.stage * raw.bytes;
+    if (pos >= it.q) {
+      mbar_arrive(full);
+      continue;
+    }
+    const uint8_t* rec = record_ptr(L, it.b, it.h, pos / G);
+    const uint32_t rb = (uint32_t)L.record_bytes;
+    if (G == 32) {
+      const bool two = pos + 32 < it.q;
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "r"(two ? 2 * rb : rb) : "memory");
+      bulk_g2s(dst, rec, rb, full);
+      if (two) bulk_g2s(dst + rb, record_ptr(L, it.b, it.h, pos / G + 1), rb, full);
     } else {
-      at += step;
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "r"(raw.tile + L.tile_bytes) : "memory");
+      if (raw.tile) bulk_g2s(dst, rec + L.rec_ksz_off, kD * 4, full);
+      bulk_g2s(dst + raw.tile, rec + L.tile0_off + (G == 128 ? ((pos >> 6) & 1) * L.tile_bytes : 0), L.tile_bytes, full);
     }
   }
-  // 32-token blocks: the part's second block
-  __device__ __forceinline__ const uint8_t* second(const LayerView& L) const {
-    return in_page + 1 < per_page ? at + L.record_bytes : find(block + 1, L) + offset;
-  }
-};
-
-// 64 key codes of one channel in token order, with the scales of their one or
-// two blocks.
-template <int KB>
-struct KeyRow {
-  uint32_t w[2 * KB];
-  uint32_t sz[2];  // per channel: (scale, zero) of tokens 0-31 and 32-63
-};
-// What a producer thread keeps per channel: byte offsets inside a tile.
-struct KeyChannel {
-  int codes, x;    // the channel's row, its chunk swizzle
-  int sz;          // per channel: its (scale, zero) pair in the record or tile
-};
-template <int KB>
-__device__ __forceinline__ KeyChannel key_channel(const LayerView& L, int d) {
-  KeyChannel c;
-  const bool wide = L.group_k >= 64;
-  c.x = wide ? chunk_swizzle(d, KB / 2) : KB == 8 ? chunk_swizzle(d, 2) : 0;
-  c.codes = L.kc_off + 4 * (wide ? d * 2 * KB : KB == 2 ? kc_word_index(d, 0, 2) : d * KB);
-  c.sz = (L.rec_ksz_off >= 0 ? L.rec_ksz_off - L.tile0_off : L.ksz_off) + 4 * d;
-  return c;
-}
-// Loads the channel's row of the cursor's part; `valid` tokens of it exist
-// (<= 0, 32 or >= 64).
-template <int KB>
-__device__ __forceinline__ void load_key_row(const LayerView& L, const PartCursor& cur, int valid, const KeyChannel& c,
-                                             bool wide, bool axis0, KeyRow<KB>& r) {
-  if (valid <= 0) return;
-  const uint8_t* tp = cur.at;
-  if (wide) {
-    const uint8_t* kc = tp + c.codes;
-#pragma unroll
-    for (int e = 0; e < KB / 2; ++e) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(kc + ((e ^ c.x) << 4)));
-      r.w[4 * e] = v.x, r.w[4 * e + 1] = v.y, r.w[4 * e + 2] = v.z, r.w[4 * e + 3] = v.w;
-    }
-    // (128-token blocks keep a channel's scales once, before the first tile)
-    if (axis0) r.sz[0] = __ldg(reinterpret_cast<const uint32_t*>(tp + (L.rec_ksz_off >= 0 ? L.tile0_off - cur.offset : 0) + c.sz));
-    r.sz[1] = r.sz[0];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (e == 1) {
-        if (valid <= 32) {
-#pragma unroll
-          for (int i = 0; i < KB; ++i) r.w[KB + i] = 0u;
-          r.sz[1] = 0u;
-          break;
-        }
-        tp = cur.second(L);
-      }
-      if constexpr (KB == 2) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(tp + c.codes));
-        r.w[2 * e] = v.x, r.w[2 * e + 1] = v.y;
-      } else {
-#pragma unroll
-        for (int i = 0; i < KB / 4; ++i) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(tp + c.codes) + (i ^ c.x));
-          r.w[KB * e + 4 * i] = v.x, r.w[KB * e + 4 * i + 1] = v.y, r.w[KB * e + 4 * i + 2] = v.z,
-                          r.w[KB * e + 4 * i + 3] = v.w;
-        }
-      }
-      if (axis0) r.sz[e] = __ldg(reinterpret_cast<const uint32_t*>(tp + c.sz));
-    }
-  }
-}
-// Per-channel keys.
-template <int KB>
-__device__ __forceinline__ void store_key_row(const KeyRow<KB>& r, uint32_t row, int d) {
-  uint32_t s[2], z[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    s[e] = __byte_perm(r.sz[e], r.sz[e], 0x1010);
-    z[e] = __byte_perm(r.sz[e], r.sz[e], 0x3232);
-  }
-  expand_row<KB, false>(r.w, row, d & 7, [&](int pair, uint32_t& s2, uint32_t& z2) {
-    s2 = s[pair >> 4];
-    z2 = z[pair >> 4];
-  });
-}
-// Per-token keys: the (scale, zero) pairs of the channel's group, of tokens 0
-// .. 31 at tok and 32 .. 63 at tok2, are the same for every lane.
-template <int KB>
-__device__ __forceinline__ void store_key_row_per_token(const KeyRow<KB>& r, uint32_t row, int d, const uint8_t* tok,
-                                                        const uint8_t* tok2, int stride) {
-  constexpr int per = 32 / KB, pairs = per / 2;
-  expand_row<KB, false>(r.w, row, d & 7, [&](int pair, uint32_t& s2, uint32_t& z2) {
-    const int base = (pair / pairs) * per, a = base + code_at(2 * (pair % pairs), per),
-              c = base + code_at(2 * (pair % pairs) + 1, per);
-    const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>((a < 32 ? tok : tok2) + (a & 31) * stride));
-    const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>((c < 32 ? tok : tok2) + (c & 31) * stride));
-    s2 = __byte_perm(u, v, 0x5410);
-    z2 = __byte_perm(u, v, 0x7632);
-  });
+  return true;
 }
 
-struct Bars {
-  uint32_t k_full, k_empty, v_full, v_empty, s_full, p_ready, pv_done, q_ready, drain;  // addresses of arrays of barriers
-};
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds2(uint32_t addr) {
+  unsigned short v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
 
-// Key tiles of phase A: thread kt expands channels kt % 64 and kt % 64 + 64 of
-// the 64-token part kt / 64 of a tile, one row after the other; a row is loaded
-// while the one before it is expanded.
+// The warp has read what it needs of the stage.
+__device__ __forceinline__ void release_raw(const Bars& bar, const RawRing& ring) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar.raw_empty + 8 * ring.stage);
+}
+
+// Key tiles of phase A: thread kt expands channel kt of a part.
 template <int KB>
 __device__ bool produce_keys(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, int kt,
                              volatile int* abort) {
-  const int tiles = min(it.k1, it.nA) - it.k0;
-  if (tiles <= 0) return true;
+  const int parts = 2 * (min(it.k1, it.nA) - it.k0);
+  if (parts <= 0) return true;
   const LayerView& L = p.L;
   const bool axis0 = L.k_axis == 0, wide = L.group_k >= 64;
-  const int part = kt >> 6, d0 = kt & 63;
-  const KeyChannel ch = key_channel<KB>(L, d0);
-  const int up = key_channel<KB>(L, 64).codes - key_channel<KB>(L, 0).codes;  // to channel d + 64 (same swizzle)
-  PartCursor cur;
-  cur.init(L, it.b, it.h, it.q, 2 * (it.a0 + it.k0) + part);
-  int valid = it.q - (it.a0 + it.k0) * kTile - 64 * part;  // positions of the part that exist, and of those after it
-  KeyRow<KB> row, next;
-  load_key_row<KB>(L, cur, valid, ch, wide, axis0, next);
-  const int stride = 4 * (kD / L.group_v);
-  const uint32_t dst = smem + kKOff + part * kHalf + d0 * 128;
+  const RawLayout raw(L);
+  RawRing ring(raw.stages);
+  // the channel's codes (64-token tiles: a row of KB / 2 chunks; 32-token
+  // blocks: the same words in two blocks), its scales or its group's
+  const int x = wide ? chunk_swizzle(kt, KB / 2) : KB == 8 ? chunk_swizzle(kt, 2) : 0;
+  const int codes = raw.tile + L.kc_off + 4 * (wide ? kt * 2 * KB : KB == 2 ? kc_word_index(kt, 0, 2) : kt * KB);
+  const int sz = raw.tile ? 4 * kt : L.ksz_off + 4 * kt;
+  const int block = wide ? 0 : (int)L.record_bytes;
+  const int tok = raw.tile + L.ksz_off + 4 * (kt / L.group_v), ng = kD / L.group_v;
+  const int tok2 = wide ? tok + 32 * 4 * ng : tok + block;
+  int valid = it.q - (it.a0 + it.k0) * kTile;  // positions of the part that exist, and of those after it
+  const uint32_t dst = smem + kKOff + kt * 128;
   int st = 0;
   uint32_t phase = 1;  // of the stage's empty barrier: the first pass does not wait
 #pragma unroll 1
-  for (int u = 0; u < 2 * tiles; ++u) {
-    const int e = u & 1;  // channel d0 + 64 e
-    row = next;
-    const int here = valid;
-    const uint8_t *tok = cur.at, *tok2 = cur.at;
-    if (!axis0 && here > 0) {
-      const int at = L.ksz_off + 4 * ((d0 + 64 * e) / L.group_v);
-      tok = cur.at + at;
-      tok2 = wide ? tok + 32 * stride : here > 32 ? cur.second(L) + at : tok;
+  for (int u = 0; u < parts; ++u, valid -= 64, ring.next()) {
+    if (!mbar_wait_warp(bar.raw_full + 8 * ring.stage, ring.parity, abort)) return false;
+    const uint32_t src = smem + kRawOff + ring.stage * raw.bytes;
+    uint32_t w[2 * KB], s[2], z[2];
+    if (wide) {
+#pragma unroll
+      for (int e = 0; e < KB / 2; ++e) {
+        const uint4 v = lds16(src + codes + ((e ^ x) << 4));
+        w[4 * e] = v.x, w[4 * e + 1] = v.y, w[4 * e + 2] = v.z, w[4 * e + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if constexpr (KB == 2) {
+          w[2 * b] = lds4(src + codes + b * block);
+          w[2 * b + 1] = lds4(src + codes + b * block + 4);
+        } else {
+#pragma unroll
+          for (int e = 0; e < KB / 4; ++e) {
+            const uint4 v = lds16(src + codes + b * block + ((e ^ x) << 4));
+            w[KB * b + 4 * e] = v.x, w[KB * b + 4 * e + 1] = v.y, w[KB * b + 4 * e + 2] = v.z,
+                           w[KB * b + 4 * e + 3] = v.w;
+          }
+        }
+      }
     }
-    if (e) {
-      cur.next(L);
-      valid -= kTile;
+    if (axis0) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t v = lds4(src + sz + b * block);
+        s[b] = __byte_perm(v, v, 0x1010);
+        z[b] = __byte_perm(v, v, 0x3232);
+      }
     }
-    KeyChannel c = ch;
-    c.codes += e ? 0 : up;
-    c.sz += e ? 0 : 256;
-    load_key_row<KB>(L, cur, u + 1 < 2 * tiles ? valid : 0, c, wide, axis0, next);
-    if (!e && !mbar_wait_warp(bar.k_empty + 8 * st, phase, abort)) return false;
-    const uint32_t at = dst + st * kTileBytes + e * (64 * 128);
-    if (here <= 0) zero_row(at);
-    else if (axis0) store_key_row<KB>(row, at, d0);
-    else store_key_row_per_token<KB>(row, at, d0, tok, tok2, stride);
-    if (e) {
+    if (axis0) release_raw(bar, ring);
+    if (!(u & 1) && !mbar_wait_warp(bar.k_empty + 8 * st, phase, abort)) return false;
+    const uint32_t row = dst + st * kTileBytes + (u & 1) * kHalf;
+    if (valid <= 0) {
+      zero_row(row);
+    } else if (axis0) {
+      expand_row<KB, false>(w, row, kt & 7, [&](int, int pair, uint32_t& s2, uint32_t& z2) {
+        s2 = s[pair >> 4];
+        z2 = z[pair >> 4];
+      });
+    } else {
+      // per-token keys: the (scale, zero) of each token, the same for a group's
+      // channels (a second block that is not there leaves what the stage held:
+      // its tokens are hidden)
+      constexpr int per = 32 / KB;
+      uint32_t t[per];
+      expand_row<KB, false>(w, row, kt & 7, [&](int word, int pair, uint32_t& s2, uint32_t& z2) {
+        const int i = pair % (per / 2);
+        if (i == 0) {
+          const uint32_t at = src + (word < KB ? tok + word * per * 4 * ng : tok2 + (word - KB) * per * 4 * ng);
+          if (ng == 1) {
+#pragma unroll
+            for (int e = 0; e < per; e += 4) {
+              const uint4 v = lds16(at + 4 * e);
+              t[e] = v.x, t[e + 1] = v.y, t[e + 2] = v.z, t[e + 3] = v.w;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < per; ++e) t[e] = lds4(at + 4 * e * ng);
+          }
+        }
+        const uint32_t a = t[code_at(2 * i, per)], c = t[code_at(2 * i + 1, per)];
+        s2 = __byte_perm(a, c, 0x5410);
+        z2 = __byte_perm(a, c, 0x7632);
+      });
+    }
+    if (!axis0) release_raw(bar, ring);
+    if (u & 1) {
       fence_async_smem();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive(bar.k_full + 8 * st);
@@ -563,89 +567,78 @@ __device__ bool produce_keys(const ChunkParams& p, const Item& it, uint32_t smem
   return true;
 }
 
-// 64 value codes (channels 64 * half ..) of one token.
-template <int VB>
-struct ValueRow {
-  uint32_t w[2 * VB];
-  uint32_t sz[2];  // (scale, zero) of the first and second 32 channels
-};
-// Value tiles of phase A: thread vt expands token vt of a tile, one 64-channel
-// half after the other, into the keys' token order; loads as for the keys.
+// Token of a 64-token part that value thread i of 64 expands. Eight lanes in a
+// row read stored rows that differ in their last three bits and write places
+// that do, so that neither the loads nor the stores conflict:
+//  * key words of per codes: stored row (t % c) (T / c) + t / c, c = per / 2,
+//    place 2 (t % c) + (t / c) % 2 (c = 2: t itself) in its group of per;
+//  * 32-token blocks with 2-bit keys: their own order (vc_row).
+__device__ __forceinline__ int value_token(int i, int kb, bool pair32) {
+  const int l = i & 7, j = i >> 3;
+  if (pair32) return 32 * (j >> 2) + 8 * (l >> 1) + (l & 1) + 2 * ((j + (l >> 2)) & 3);
+  const int c = 16 / kb;
+  return c * (l + 8 * (j / c)) + ((j + (kb == 8 ? l >> 2 : l >> 1)) & (c - 1));
+}
+// Value tiles of phase A: thread vt expands half vt / 64 (64 channels) of a
+// token of a part, into the keys' token order.
 template <int VB>
 __device__ bool produce_values(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, int vt,
                                volatile int* abort) {
-  const int tiles = min(it.k1, it.nA) - it.k0;
-  if (tiles <= 0) return true;
+  const int parts = 2 * (min(it.k1, it.nA) - it.k0);
+  if (parts <= 0) return true;
   const LayerView& L = p.L;
-  const int per = 32 / L.k_bits;
-  const int place = (vt & ~(per - 1)) + place_of(vt & (per - 1), per);
-  // the thread's token inside a tile part: its code row, and its scales' places
-  const int TT = L.tile_tokens, t = vt & (TT - 1), ng = kD / L.group_v;
+  const RawLayout raw(L);
+  RawRing ring(raw.stages);
+  const int per = 32 / L.k_bits, half = vt >> 6;
+  const int tok = value_token(vt & 63, L.k_bits, pair_layout(L.group_k, L.k_bits));
+  const int place = (tok & ~(per - 1)) + place_of(tok & (per - 1), per);
+  // where its codes and scales sit in a stage
+  const int TT = L.tile_tokens, t = tok & (TT - 1), ng = kD / L.group_v;
+  const int tile = raw.tile + (TT == 32 && tok >= 32 ? (int)L.record_bytes : 0);
   const int crow = vc_row(t, TT, L.k_bits), x = chunk_swizzle(crow, VB);
-  const int codes = L.vc_off + crow * VB * 16;
-  const bool fine = L.group_v < 64, second = TT == 32 && (vt & 32);
-  auto scale_at = [&](int g) {  // offset of the scale of 32-channel group g
-    return L.vsz_off + 2 * vsz_half_index(t, 32 * g / L.group_v, TT, L.k_bits, ng, false);
-  };
-  const int sz0 = scale_at(0), sz2 = scale_at(2), fine_step = scale_at(1) - sz0;  // (groups are evenly spaced)
-  const int zo = vsz_half_index(t, 0, TT, L.k_bits, ng, true) - vsz_half_index(t, 0, TT, L.k_bits, ng, false);
-  PartCursor cur;
-  cur.init(L, it.b, it.h, it.q, 2 * (it.a0 + it.k0) + (vt >> 6));
-  int valid = it.q - (it.a0 + it.k0) * kTile - vt;  // > 0: the thread's token exists
-  const uint8_t* tp = nullptr;                      // its tile
-  ValueRow<VB> row, next;
-  auto load = [&](int half) {
-    const uint8_t* vc = tp + codes;
+  const int codes = tile + L.vc_off + crow * VB * 16;
+  int sz[2], zo[2];  // scale and zero point of the half's 32-channel groups
 #pragma unroll
-    for (int e = 0; e < VB / 2; ++e) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(vc + (((half * (VB / 2) + e) ^ x) << 4)));
-      next.w[4 * e] = v.x, next.w[4 * e + 1] = v.y, next.w[4 * e + 2] = v.z, next.w[4 * e + 3] = v.w;
-    }
-    const unsigned short* sz = reinterpret_cast<const unsigned short*>(tp + (half ? sz2 : sz0));
-    next.sz[0] = (uint32_t)__ldg(sz) | ((uint32_t)__ldg(sz + zo) << 16);
-    next.sz[1] = next.sz[0];
-    if (fine) {
-      sz += fine_step / 2;
-      next.sz[1] = (uint32_t)__ldg(sz) | ((uint32_t)__ldg(sz + zo) << 16);
-    }
-  };
-  if (valid > 0) {
-    tp = second ? cur.second(L) : cur.at;
-    load(0);
+  for (int e = 0; e < 2; ++e) {
+    const int g = (64 * half + 32 * e) / L.group_v;
+    sz[e] = tile + L.vsz_off + 2 * vsz_half_index(t, g, TT, L.k_bits, ng, false);
+    zo[e] = tile + L.vsz_off + 2 * vsz_half_index(t, g, TT, L.k_bits, ng, true);
   }
-  const uint32_t dst = smem + kVOff + place * 128;
+  int valid = it.q - (it.a0 + it.k0) * kTile - tok;  // > 0: the thread's token exists
+  const uint32_t dst = smem + kVOff + half * kHalf + place * 128;
   int st = 0;
   uint32_t phase = 1;
 #pragma unroll 1
-  for (int u = 0; u < 2 * tiles; ++u) {
-    const int e = u & 1;
-    row = next;
-    const bool here = valid > 0;
-    if (e) {
-      cur.next(L);
-      valid -= kTile;
-    }
-    if (u + 1 < 2 * tiles && valid > 0) {
-      if (e) tp = second ? cur.second(L) : cur.at;
-      load(e ^ 1);
-    }
-    if (!e && !mbar_wait_warp(bar.v_empty + 8 * st, phase, abort)) return false;
-    const uint32_t at = dst + st * kTileBytes + e * kHalf;
-    if (!here) {
-      zero_row(at);
-    } else {
-      uint32_t s[2], z[2];
+  for (int u = 0; u < parts; ++u, valid -= 64, ring.next()) {
+    if (!mbar_wait_warp(bar.raw_full + 8 * ring.stage, ring.parity, abort)) return false;
+    const uint32_t src = smem + kRawOff + ring.stage * raw.bytes;
+    uint32_t w[2 * VB], s[2], z[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        s[i] = __byte_perm(row.sz[i], row.sz[i], 0x1010);
-        z[i] = __byte_perm(row.sz[i], row.sz[i], 0x3232);
-      }
-      expand_row<VB, true>(row.w, at, place & 7, [&](int pair, uint32_t& s2, uint32_t& z2) {
+    for (int e = 0; e < VB / 2; ++e) {
+      const uint4 v = lds16(src + codes + (((half * (VB / 2) + e) ^ x) << 4));
+      w[4 * e] = v.x, w[4 * e + 1] = v.y, w[4 * e + 2] = v.z, w[4 * e + 3] = v.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t a = lds2(src + sz[e]), b = lds2(src + zo[e]);
+      s[e] = __byte_perm(a, a, 0x1010);
+      z[e] = __byte_perm(b, b, 0x1010);
+    }
+    // (before the wait: with a single raw stage the keys of this tile may still
+    // have to pass through it, and the product that frees a value stage is
+    // issued after the next scores)
+    release_raw(bar, ring);
+    if (!(u & 1) && !mbar_wait_warp(bar.v_empty + 8 * st, phase, abort)) return false;
+    const uint32_t row = dst + st * kTileBytes + (u & 1) * (64 * 128);
+    if (valid <= 0) {
+      zero_row(row);
+    } else {
+      expand_row<VB, true>(w, row, place & 7, [&](int, int pair, uint32_t& s2, uint32_t& z2) {
         s2 = s[pair >> 4];
         z2 = z[pair >> 4];
       });
     }
-    if (e) {
+    if (u & 1) {
       fence_async_smem();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive(bar.v_full + 8 * st);
@@ -677,7 +670,10 @@ __device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t til
   const int slot0 = it.q % L.residual;  // ring slot of the first ring token
   for (int k = max(it.k0, it.nA); k < it.k1; ++k) {
     const int c = k - it.k0, st = c % STAGES, e0 = it.tile_b(k) * kTile;
-    if (c >= STAGES && !mbar_wait_warp(empty + 8 * st, ((c / STAGES) - 1) & 1, abort)) return false;
+    if (c >= STAGES && !mbar_wait_warp(empty + 8 * st, ((c / STAGES) - 1) & 1, abort)) {
+      for (int v = c - STAGES; v < c; ++v) mbar_drain(full + 8 * (v % STAGES), (v / STAGES) & 1);
+      return false;
+    }
     const uint32_t dst = tiles + st * kTileBytes, bar = full + 8 * st;
     if (e0 >= held && e0 - held + kTile <= p.t_new[it.i]) {
       if ((kt & 31) == 0) {
@@ -1132,6 +1128,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
     bar.p_ready = at, at += 16;
     bar.pv_done = at, at += 16;
     bar.q_ready = at, at += 16;
+    bar.raw_full = at, at += 8 * kRawStages;
+    bar.raw_empty = at, at += 8 * kRawStages;
     bar.drain = at;
   }
   if (threadIdx.x == 0) {
@@ -1148,6 +1146,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
       mbar_init(bar.p_ready + 8 * i, 4);
       mbar_init(bar.pv_done + 8 * i, 1);
       mbar_init(bar.q_ready + 8 * i, 4);
+    }
+    for (int i = 0; i < kRawStages; ++i) {
+      mbar_init(bar.raw_full + 8 * i, 1);
+      mbar_init(bar.raw_empty + 8 * i, 2 * kProducers / 32);
     }
     mbar_init(bar.drain, 1);
     s_abort = 0;
@@ -1190,11 +1192,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
       if (!issue_products(p, it, smem, tmem, bar, abort)) {
         // let the products in flight finish before the tensor memory goes
         tc_commit(bar.drain);
-        const long long t0 = clock64();
-        while (!mbar_try(bar.drain, 0) && clock64() - t0 < kWaitCycles) {
-        }
+        mbar_drain(bar.drain, 0);
       }
     }
+    if (warp == 17 && (threadIdx.x & 31) == 0) (void)copy_parts(p, it, smem, bar, abort);
     __syncwarp();
   }
   tc_before();
