@@ -112,6 +112,12 @@ __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
+// One lane of the (converged) warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
+}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -210,18 +216,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-// Shared-memory descriptors: start >> 4, leading and stride byte offsets >> 4,
-// version 1 (bit 46), 128-byte swizzle (2 at bit 61). K-major tiles: rows of
-// 64 k-elements (128 bytes), 8-row groups 1024 bytes apart. MN-major tiles:
-// rows of 64 mn-elements, one k each, 8-k groups 1024 bytes apart and the
-// second 64 mn-elements kHalf further.
-__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(kHalf >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
-}
 // Instruction descriptor: fp32 accumulator, A and B f16 or bf16, B MN-major or
 // K-major, N = M = 128.
 __device__ __forceinline__ uint32_t inst_desc(bool bf16, bool b_mn) {
@@ -839,26 +833,54 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// The state of one row's softmax, and one chunk of 32 columns (loaded in s) of
-// a tile: the maximum, a rescaling where it is due, the probabilities as packed
-// pairs over the columns 16q .. of the scores already read.
+// The state of one row's softmax.
 struct RowState {
   float m = -INFINITY;  // a whole number, or -inf
   float l = 0.f;
 };
+// Packed probabilities 2^(s cs + bias) of 32 columns, and their sum.
 template <bool BF16>
-__device__ __forceinline__ void softmax_chunk(uint32_t (&s)[32], int q, float cs, RowState& st, uint32_t tm_s,
-                                              uint32_t tm_o, bool have_o) {
-  float mx = __uint_as_float(s[0]);
+__device__ __forceinline__ float probabilities(const uint32_t (&s)[32], float cs, float bias, uint32_t (&w)[16]) {
+  const uint64_t cs2 = pair_of(cs, cs), b2 = pair_of(bias, bias);
+  uint64_t sum = 0;
 #pragma unroll
-  for (int c = 1; c < 31; c += 2) mx = max3(mx, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-  mx = fmaxf(mx, __uint_as_float(s[31])) * cs;
-  const bool grow = mx > st.m + kLazy;
-  if (__any_sync(0xffffffffu, grow)) {
-    const float m = grow ? ceilf(mx) : st.m;
+  for (int c = 0; c < 16; ++c) {
+    float a, b;
+    unpair(fma2(pair_of(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), cs2, b2), a, b);
+    a = ex2(a);
+    b = ex2(b);
+    sum = add2(sum, pair_of(a, b));
+    w[c] = pack2<BF16>(a, b);
+  }
+  float a, b;
+  unpair(sum, a, b);
+  return a + b;
+}
+// One chunk of 32 columns (scores in s) of a tile. The probabilities go by the
+// m so far, so that nothing waits for the chunk's maximum; where that turns
+// out to pass m by more than kLazy (always on a row's first chunk), m is
+// raised, what was written is rescaled and the chunk is computed again. Packed
+// pairs go over the columns 16q .. of the scores already read.
+template <bool BF16>
+__device__ __forceinline__ void softmax_chunk(const uint32_t (&s)[32], int q, float cs, RowState& st, uint32_t tm_s,
+                                              uint32_t tm_o, bool have_o) {
+  uint32_t w[16];
+  float sum = probabilities<BF16>(s, cs, kOffset - st.m, w);
+  float mx[2] = {__uint_as_float(s[0]), __uint_as_float(s[1])};
+#pragma unroll
+  for (int c = 2; c < 30; c += 4) {
+    mx[0] = max3(mx[0], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+    mx[1] = max3(mx[1], __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+  }
+  const float top = max3(mx[0], mx[1], fmaxf(__uint_as_float(s[30]), __uint_as_float(s[31]))) * cs;
+  const bool grow = top > st.m + kLazy;
+  // (a row that has seen nothing yet computes 2^(-inf + inf): again, as zeros)
+  if (__any_sync(0xffffffffu, grow || st.m == -INFINITY)) {
+    const float m = grow ? ceilf(top) : st.m;
     const float a = grow ? ex2(st.m - m) : 1.f;  // a power of two; 0 while m = -inf
     st.m = m;
     st.l *= a;
+    sum = probabilities<BF16>(s, cs, m == -INFINITY ? 0.f : kOffset - m, w);
     // the slot's previous product is complete (its scores' barrier completed
     // after it), and so O is at rest; the tile's own probabilities so far too
     tmem_wait_st();
@@ -875,36 +897,21 @@ __device__ __forceinline__ void softmax_chunk(uint32_t (&s)[32], int q, float cs
     }
 #pragma unroll 1
     for (int c = 0; c < q; ++c) {
-      uint32_t w[16];
-      tmem_ld16(tm_s + 16 * c, w);
-      tmem_wait_ld16(w);
+      uint32_t o[16];
+      tmem_ld16(tm_s + 16 * c, o);
+      tmem_wait_ld16(o);
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         float2 f;
-        if constexpr (BF16) f = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
-        else f = __half22float2(half2_of(w[e]));
-        w[e] = pack2<BF16>(f.x * a, f.y * a);
+        if constexpr (BF16) f = make_float2(__uint_as_float(o[e] << 16), __uint_as_float(o[e] & 0xffff0000u));
+        else f = __half22float2(half2_of(o[e]));
+        o[e] = pack2<BF16>(f.x * a, f.y * a);
       }
-      tmem_st16(tm_s + 16 * c, w);
+      tmem_st16(tm_s + 16 * c, o);
     }
   }
-  const float bias = st.m == -INFINITY ? 0.f : kOffset - st.m;
-  const uint64_t cs2 = pair_of(cs, cs), b2 = pair_of(bias, bias);
-  uint64_t sum = 0;
-  uint32_t w[16];
-#pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    float a, b;
-    unpair(fma2(pair_of(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), cs2, b2), a, b);
-    a = ex2(a);
-    b = ex2(b);
-    sum = add2(sum, pair_of(a, b));
-    w[c] = pack2<BF16>(a, b);
-  }
   tmem_st16(tm_s + 16 * q, w);
-  float a, b;
-  unpair(sum, a, b);
-  st.l += a + b;
+  st.l += sum;
 }
 // Scores whose bit is clear become -inf.
 __device__ __forceinline__ void mask_chunk(uint32_t (&s)[32], uint32_t bits) {
@@ -1041,71 +1048,101 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
   return true;
 }
 
-// One thread issues every product of the item, in the order S(0), S(1), then
+// Shared-memory descriptors: start >> 4, leading and stride byte offsets >> 4,
+// version 1 (bit 46), 128-byte swizzle (2 at bit 61). K-major tiles: rows of
+// 64 k-elements (128 bytes), 8-row groups 1024 bytes apart. MN-major tiles:
+// rows of 64 mn-elements, one k each, 8-k groups 1024 bytes apart and the
+// second 64 mn-elements kHalf further. They differ in the low word only.
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride, version, swizzle
+constexpr uint32_t kDescK = 1u << 16, kDescMn = (uint32_t)(kHalf >> 4) << 16;  // leading offset
+// The eight k-steps of one slot's scores (MN: expanded keys, else exact ones)
+// and of its product with the values.
+template <bool MN>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q_lo, uint32_t k_lo, uint32_t id) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    constexpr int kStep = 2048 >> 4;
+    const int step = ((e >> 2) * kHalf + (e & 3) * 32) >> 4;
+    mma_ss(d, desc_of(q_lo + step, kDescHi), desc_of(k_lo + (MN ? e * kStep : step), kDescHi), id, e > 0);
+  }
+}
+__device__ __forceinline__ void issue_values(uint32_t d, uint32_t p, uint32_t v_lo, uint32_t id, bool acc) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) mma_ts(d, p + 8 * e, desc_of(v_lo + e * (2048 >> 4), kDescHi), id, acc || e > 0);
+}
+
+// One warp issues every product of the item (by one elected lane; the warp
+// walks the loop together, so that descriptors are warp-uniform values), in the
+// order S(0), S(1), then
 // P V of step v and S of step v + 2: a slot's next scores are queued behind
 // its own product (which reads the P they overwrite) while the other slot's
-// softmax runs.
+// softmax runs. The tensor cores idle while this thread does anything else, so
+// a step is kept short: what it needs is counted, not worked out.
 __device__ bool issue_products(const ChunkParams& p, const Item& it, uint32_t smem, uint32_t tmem, const Bars& bar,
                                volatile int* abort) {
   const int steps = it.steps();
-  const bool bf16 = p.L.kv_dtype == KVQ_BF16;
-  // what the scores of step v need: the slot's query, the tile's keys
-  auto wait_scores = [&](int v) -> bool {
-    const int w = v & 1, c = it.both ? v >> 1 : v, k = it.k0 + c, st = c % kKStages;
-    const int j = v >> 1;
-    const bool enter_b = k >= it.nA && (j == 0 || it.slot_tile(w, j - 1) < it.nA);
-    if ((j == 0 || enter_b) && !mbar_wait(bar.q_ready + 8 * w, j == 0 ? 0 : 1, abort)) return false;
-    return (it.both && w == 1) || mbar_wait(bar.k_full + 8 * st, (c / kKStages) & 1, abort);
-  };
-  auto scores = [&](int v) {
-    const int w = v & 1, c = it.both ? v >> 1 : v, k = it.k0 + c, st = c % kKStages;
-    const bool in_a = k < it.nA;
-    const uint32_t q = smem + kQOff + w * kTileBytes, kt = smem + kKOff + st * kTileBytes;
-    const uint32_t d = tmem + kTmemS + w * kTile;
-    const uint32_t id = inst_desc(!in_a && bf16, in_a);
-    const uint64_t a = desc_k(q), b = in_a ? desc_mn(kt) : desc_k(kt);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint64_t step = ((e >> 2) * kHalf + (e & 3) * 32) >> 4;
-      mma_ss(d, a + step, b + (in_a ? (uint64_t)(e * 2048 >> 4) : step), id, e > 0);
+  const bool leader = elect_one();
+  const bool bf16 = p.L.kv_dtype == KVQ_BF16, both = it.both;
+  const uint32_t q_lo = ((smem + kQOff) >> 4) | kDescK;
+  const uint32_t k_base = (smem + kKOff) >> 4, v_lo = ((smem + kVOff) >> 4) | kDescMn;
+  const uint32_t id_a = inst_desc(false, true), id_bk = inst_desc(bf16, false), id_bv = inst_desc(bf16, true);
+  constexpr uint32_t kTileLo = kTileBytes >> 4;
+  static_assert(kKStages == 2 && kVStages == 2, "stages are counted in one bit");
+  const int first_b = it.nA - it.k0;  // tiles of the item before phase B
+  // tile n of the item (counted from k0) sits in stage n % 2, in phase n / 2
+  auto scores = [&](int w, int n) {
+    const uint32_t lo = k_base + (n & 1) * kTileLo, d = tmem + kTmemS + w * kTile, q = q_lo + w * kTileLo;
+    if (n < first_b) {
+      if (leader) issue_scores<true>(d, q, lo | kDescMn, id_a);
+    } else {
+      if (leader) issue_scores<false>(d, q, lo | kDescK, id_bk);
     }
-    tc_commit(bar.s_full + 8 * w);
-    if (!it.both || w == 1) tc_commit(bar.k_empty + 8 * st);
-  };
-  auto values = [&](int v) {
-    const int w = v & 1, c = it.both ? v >> 1 : v, k = it.k0 + c, st = c % kVStages, j = v >> 1;
-    const uint32_t pa = tmem + kTmemS + w * kTile, d = tmem + kTmemO + w * kD;
-    const uint32_t id = inst_desc(k >= it.nA && bf16, true);
-    const uint64_t b = desc_mn(smem + kVOff + st * kTileBytes);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) mma_ts(d, pa + 8 * e, b + (uint64_t)(e * 2048 >> 4), id, j > 0 || e > 0);
-    tc_commit(bar.pv_done + 8 * w);
-    if (!it.both || w == 1) tc_commit(bar.v_empty + 8 * st);
+    if (leader) tc_commit(bar.s_full + 8 * w);
+    if (leader && (!both || w == 1)) tc_commit(bar.k_empty + 8 * (n & 1));
+    __syncwarp();
   };
   for (int v = 0; v < 2 && v < steps; ++v) {
-    if (!wait_scores(v)) return false;
+    const int n = both ? 0 : v;
+    if (!mbar_wait_warp(bar.q_ready + 8 * v, 0, abort)) return false;
+    if (!mbar_wait_warp(bar.k_full + 8 * (n & 1), 0, abort)) return false;
     tc_after();
-    scores(v);
+    scores(v, n);
   }
+  int n = 0;  // tile of step v; the slot's next tile is n + ahead
+  const int ahead = both ? 1 : 2;
 #pragma unroll 1
   for (int v = 0; v < steps; ++v) {
-    const int w = v & 1, c = it.both ? v >> 1 : v, st = c % kVStages;
+    const int w = v & 1, next = n + ahead;
+    const bool more = v + 2 < steps;
     // a slot that enters phase B rewrites its query only after this product
-    const bool next = v + 2 < steps;
-    const int kn = it.slot_tile(w, (v >> 1) + 1);
-    const bool enter_b = next && kn >= it.nA && it.k0 + c < it.nA;
-    if ((!it.both || w == 0) && !mbar_wait(bar.v_full + 8 * st, (c / kVStages) & 1, abort)) return false;
-    if (next && !enter_b && !wait_scores(v + 2)) return false;
-    if (!mbar_wait(bar.p_ready + 8 * w, (v >> 1) & 1, abort)) return false;
+    const bool enter_b = more && next >= first_b && n < first_b;
+    if (!both || w == 0) {
+      if (!mbar_wait_warp(bar.v_full + 8 * (n & 1), (n >> 1) & 1, abort)) return false;
+      if (more && !mbar_wait_warp(bar.k_full + 8 * (next & 1), (next >> 1) & 1, abort)) return false;
+    }
+    if (!mbar_wait_warp(bar.p_ready + 8 * w, (v >> 1) & 1, abort)) return false;
     tc_after();
-    values(v);
-    if (next) {
+    const uint32_t od = tmem + kTmemO + w * kD, op = tmem + kTmemS + w * kTile, ov = v_lo + (n & 1) * kTileLo;
+    const uint32_t id = n < first_b ? id_a : id_bv;
+    if (leader) {
+      issue_values(od, op, ov, id, v > 1);
+      tc_commit(bar.pv_done + 8 * w);
+    }
+    if (leader && (!both || w == 1)) tc_commit(bar.v_empty + 8 * (n & 1));
+    __syncwarp();
+    if (more) {
       if (enter_b) {
-        if (!wait_scores(v + 2)) return false;
+        if (!mbar_wait_warp(bar.q_ready + 8 * w, 1, abort)) return false;
         tc_after();
       }
-      scores(v + 2);
+      scores(w, next);
     }
+    n += both ? w : 1;
   }
   return true;
 }
@@ -1115,7 +1152,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const uint32_t smem = (smem_u32(raw) + 1023u) & ~1023u;
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   volatile int* abort = &s_abort;
   Bars bar;
   {
@@ -1188,12 +1225,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
                                     abort);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp == 16 && (threadIdx.x & 31) == 0) {
-      if (!issue_products(p, it, smem, tmem, bar, abort)) {
-        // let the products in flight finish before the tensor memory goes
-        tc_commit(bar.drain);
-        mbar_drain(bar.drain, 0);
-      }
+    if (warp == 16 && !issue_products(p, it, smem, tmem, bar, abort)) {
+      // let the products in flight finish before the tensor memory goes
+      if (elect_one()) tc_commit(bar.drain);
+      __syncwarp();
+      mbar_drain(bar.drain, 0);
+      __syncwarp();
     }
     if (warp == 17 && (threadIdx.x & 31) == 0) (void)copy_parts(p, it, smem, bar, abort);
     __syncwarp();
