@@ -838,11 +838,10 @@ struct RowState {
   float m = -INFINITY;  // a whole number, or -inf
   float l = 0.f;
 };
-// Packed probabilities 2^(s cs + bias) of 32 columns, and their sum.
+// Packed probabilities 2^(s cs + bias) of 32 columns, added to sum.
 template <bool BF16>
-__device__ __forceinline__ float probabilities(const uint32_t (&s)[32], float cs, float bias, uint32_t (&w)[16]) {
+__device__ __forceinline__ void probabilities(const uint32_t* s, float cs, float bias, uint32_t* w, uint64_t& sum) {
   const uint64_t cs2 = pair_of(cs, cs), b2 = pair_of(bias, bias);
-  uint64_t sum = 0;
 #pragma unroll
   for (int c = 0; c < 16; ++c) {
     float a, b;
@@ -852,35 +851,40 @@ __device__ __forceinline__ float probabilities(const uint32_t (&s)[32], float cs
     sum = add2(sum, pair_of(a, b));
     w[c] = pack2<BF16>(a, b);
   }
-  float a, b;
-  unpair(sum, a, b);
-  return a + b;
 }
-// One chunk of 32 columns (scores in s) of a tile. The probabilities go by the
-// m so far, so that nothing waits for the chunk's maximum; where that turns
-// out to pass m by more than kLazy (always on a row's first chunk), m is
-// raised, what was written is rescaled and the chunk is computed again. Packed
-// pairs go over the columns 16q .. of the scores already read.
+// Half a tile (64 columns, scores in s). The probabilities go by the m so far,
+// so that nothing waits for the half's maximum; where that turns out to pass m
+// by more than kLazy (always on a row's first tile), m is raised, what was
+// written is rescaled and the half is computed again. Packed pairs go over the
+// columns 32h .. of the scores already read.
 template <bool BF16>
-__device__ __forceinline__ void softmax_chunk(const uint32_t (&s)[32], int q, float cs, RowState& st, uint32_t tm_s,
-                                              uint32_t tm_o, bool have_o) {
-  uint32_t w[16];
-  float sum = probabilities<BF16>(s, cs, kOffset - st.m, w);
-  float mx[2] = {__uint_as_float(s[0]), __uint_as_float(s[1])};
+__device__ __forceinline__ void softmax_half(const uint32_t (&s)[64], int h, float cs, RowState& st, uint32_t tm_s,
+                                             uint32_t tm_o, bool have_o) {
+  uint32_t w[32];
+  uint64_t sum = 0;
+  probabilities<BF16>(s, cs, kOffset - st.m, w, sum);
+  probabilities<BF16>(s + 32, cs, kOffset - st.m, w + 16, sum);
+  float mx[4];
 #pragma unroll
-  for (int c = 2; c < 30; c += 4) {
-    mx[0] = max3(mx[0], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-    mx[1] = max3(mx[1], __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-  }
-  const float top = max3(mx[0], mx[1], fmaxf(__uint_as_float(s[30]), __uint_as_float(s[31]))) * cs;
+  for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(s[e]);
+#pragma unroll
+  for (int c = 4; c < 60; c += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[60 + e]));
+  const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
   const bool grow = top > st.m + kLazy;
-  // (a row that has seen nothing yet computes 2^(-inf + inf): again, as zeros)
+  // (a row that has seen nothing yet computed 2^(-inf + inf): again, as zeros)
   if (__any_sync(0xffffffffu, grow || st.m == -INFINITY)) {
     const float m = grow ? ceilf(top) : st.m;
     const float a = grow ? ex2(st.m - m) : 1.f;  // a power of two; 0 while m = -inf
     st.m = m;
     st.l *= a;
-    sum = probabilities<BF16>(s, cs, m == -INFINITY ? 0.f : kOffset - m, w);
+    sum = 0;
+    const float bias = m == -INFINITY ? 0.f : kOffset - m;
+    probabilities<BF16>(s, cs, bias, w, sum);
+    probabilities<BF16>(s + 32, cs, bias, w + 16, sum);
     // the slot's previous product is complete (its scores' barrier completed
     // after it), and so O is at rest; the tile's own probabilities so far too
     tmem_wait_st();
@@ -896,7 +900,7 @@ __device__ __forceinline__ void softmax_chunk(const uint32_t (&s)[32], int q, fl
       }
     }
 #pragma unroll 1
-    for (int c = 0; c < q; ++c) {
+    for (int c = 0; c < 2 * h; ++c) {
       uint32_t o[16];
       tmem_ld16(tm_s + 16 * c, o);
       tmem_wait_ld16(o);
@@ -910,33 +914,35 @@ __device__ __forceinline__ void softmax_chunk(const uint32_t (&s)[32], int q, fl
       tmem_st16(tm_s + 16 * c, o);
     }
   }
-  tmem_st16(tm_s + 16 * q, w);
-  st.l += sum;
+  tmem_st32(tm_s + 32 * h, w);
+  float a, b;
+  unpair(sum, a, b);
+  st.l += a + b;
 }
 // Scores whose bit is clear become -inf.
-__device__ __forceinline__ void mask_chunk(uint32_t (&s)[32], uint32_t bits) {
+__device__ __forceinline__ void mask_chunk(uint32_t* s, uint32_t bits) {
 #pragma unroll
   for (int e = 0; e < 32; ++e)
     if (!((bits >> e) & 1u)) s[e] = 0xff800000u;
 }
-// One tile of a row: chunks of 32 columns, the next one loading while one is
-// worked on. MASKED (some row of the item does not see all of the tile; apart
-// from the common loop): seen(c) gives the columns c .. c + 31 that the row sees.
+// One tile of a row. MASKED (some row of the item does not see all of the tile;
+// apart from the common loop): seen(c) gives the columns c .. c + 31 that the
+// row sees.
 template <bool BF16, bool MASKED, class F>
 __device__ __forceinline__ void softmax_tile(float cs, RowState& st, uint32_t tm_s, uint32_t tm_o, bool have_o,
                                              F seen) {
-  uint32_t s[2][32];
-  tmem_ld32(tm_s, s[0]);
 #pragma unroll 1
   for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int q = 2 * h + e;
-      tmem_wait_ld(s[e]);
-      if (q < 3) tmem_ld32(tm_s + 32 * (q + 1), s[e ^ 1]);
-      if constexpr (MASKED) mask_chunk(s[e], seen(32 * q));
-      softmax_chunk<BF16>(s[e], q, cs, st, tm_s, tm_o, have_o);
+    uint32_t s[64];
+    tmem_ld32(tm_s + 64 * h, s);
+    tmem_ld32(tm_s + 64 * h + 32, s + 32);
+    tmem_wait_ld(s);
+    tmem_wait_ld(s + 32);
+    if constexpr (MASKED) {
+      mask_chunk(s, seen(64 * h));
+      mask_chunk(s + 32, seen(64 * h + 32));
     }
+    softmax_half<BF16>(s, h, cs, st, tm_s, tm_o, have_o);
   }
 }
 
