@@ -480,9 +480,9 @@ kvq_status plan_chunk(const kvq_cache* c, kvq::ChunkParams& p) {
     all += units[x];
     steps += units[x] * tiles[x];
   }
-  // tiles per range: one range per SM, but at least 8 tiles (a range's start
+  // tiles per range: one range per SM, but at least 4 tiles (a range's start
   // and its merge cost about as much)
-  int64_t target = all >= sms ? INT64_MAX : std::max<int64_t>(8, (steps + sms - 1) / sms);
+  int64_t target = all >= sms ? INT64_MAX : std::max<int64_t>(4, (steps + sms - 1) / sms);
   for (bool alternate = true;; target = target > (INT64_MAX >> 2) ? INT64_MAX : target * 2) {
     int64_t items = 0, records = 0, merged = 0;
     bool fits = true;

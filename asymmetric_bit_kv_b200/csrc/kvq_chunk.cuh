@@ -58,7 +58,7 @@ cudaError_t launch_chunk_simple(const ChunkParams& p, cudaStream_t stream);
 // The tensor-core kernel and the merge of its parts: layers whose keys and
 // values share one residual length.
 constexpr int kChunkSlotRows = 128;  // query rows of one slot; a CTA has two
-constexpr int kChunkTile = 64;       // tokens of a tile
+constexpr int kChunkTile = 128;      // tokens of a tile
 bool chunk_tc_supported(const LayerView& L);
 cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream);
 

@@ -4,16 +4,14 @@
 // Method: the formula of kvq_chunk.cu. A work item is one (sequence, KV head,
 // tile of query rows); a row is (new token, query head of the KV head), so all
 // query heads of a KV head share every dequantized key and value. The item
-// walks the tokens its rows see in tiles of 64: first the quantized positions
-// (phase A, tiles of positions 64a ..), then the exact tokens (phase B: the
-// list sinks, ring, new tokens, in order). Per tile: S = Q K^T (128 x 64 x 128
+// walks the tokens its rows see in tiles of 128: first the quantized positions
+// (phase A, tiles of positions 128a ..), then the exact tokens (phase B: the
+// list sinks, ring, new tokens, in order). Per tile: S = Q K^T (128x128x128
 // per slot), online softmax, O += P V.
 //
-// Why this shape. Two slots of 128 rows use all 512 columns of tensor memory:
-// per slot two buffers of 64 score columns and O, fp32; P overwrites the scores
-// it comes from as 16-bit pairs. While a slot's softmax works on one buffer the
-// tensor cores fill the other. (Tiles of 128 tokens with one buffer per slot
-// left the softmax waiting for its own products 30% of the time.)
+// Why this shape. Two slots of 128 rows use all 512 columns of tensor memory
+// (S0 | S1 | O0 | O1, fp32; P overwrites S as 16-bit pairs) and alternate: one
+// slot's softmax runs while the tensor cores work on the other's products.
 //  * More than 128 rows: both slots walk the same tiles (256 rows share each
 //    dequantized tile).
 //  * At most 128 rows: the slots take alternate tiles, each a part of its own.
@@ -21,13 +19,13 @@
 // parts are merged by chunk_combine_kernel.
 //
 // Warps: 0-3 and 4-7 the softmax of slots 0 and 1 (a thread owns a row, so
-// maxima, sums and the rotation of a row need no exchange; two threads per row
-// measured no faster), 8, 9, 12, 13 key tiles, 10, 11, 14, 15 value tiles (each
-// kind on two of the four schedulers), 16 and 18 issue the MMAs of a slot each,
-// 17 copies packed parts (19 idle: registers move between whole warpgroups, setmaxnreg 144 +
-// 144 + 72 + 72 + 48 = 5 x 96). The hot loops are kept short (one tile, one row
-// of codes at a time): four roles share an SM's instruction caches, and
-// unrolled ones spent most of their time waiting for instructions.
+// maxima, sums and the rotation of a row need no exchange), 8, 9, 12, 13 key
+// tiles, 10, 11, 14, 15 value tiles (each kind on two of the four schedulers),
+// 16 issues the MMAs, 17 copies packed parts (18, 19 idle: registers move between
+// whole warpgroups, setmaxnreg 144 + 144 + 72 + 72 + 48 = 5 x 96). The hot
+// loops are kept short (32 columns, one row of codes at a time): four roles
+// share an SM's instruction caches, and unrolled whole tiles spent most of
+// their time waiting for instructions.
 //
 // Operands. Phase A: codes become fp16 in three instructions per pair (mask
 // into the mantissa of 1024, subtract, one fma q*d + m: the only rounding).
@@ -40,10 +38,10 @@
 // subnormals), so that any bf16 query fits fp16. Phase B: keys, values,
 // queries and probabilities in the kv dtype, keys K-major.
 // Softmax: probabilities are 2^(z - m + 6) with m a whole number that is raised
-// only when a row's maximum passes it by more than 8 (log2 units): one pass over
-// the scores; rescaling O and what the tile has written is rare and exact (powers
-// of two); fp16 probabilities reach 2^14 and keep 14 + 6 binary orders below m
-// before they turn subnormal.
+// only when the sum of 64 of a row's probabilities reaches 2^14: one pass over
+// the scores without their maximum; rescaling O and what the tile has written
+// is rare and exact (powers of two); fp16 probabilities stay below 2^14 and
+// keep 14 + 6 binary orders below m before they turn subnormal.
 //
 // Every wait is bounded (~2 s): a thread that gives up sets the device error
 // word and an abort flag that ends the others' waits.
@@ -60,20 +58,18 @@ namespace {
 constexpr int kRows = kChunkSlotRows, kTile = kChunkTile, kD = kHeadDim;
 constexpr int kThreads = 640;
 constexpr int kProducers = 128;  // threads of the key warps, and of the value warps
-constexpr int kKStages = 4, kVStages = 4;
+constexpr int kKStages = 2, kVStages = 2;
 constexpr int kRawStages = 4;           // raw stages at most
 constexpr int kTileBytes = kTile * kD * 2;
-constexpr int kHalf = kTileBytes / 2;   // one 64-channel half of a value (or exact key) tile: 64 rows of 128 bytes
-constexpr int kQBytes = kRows * kD * 2;  // one slot's queries, in two halves of 128 rows of 128 bytes
-constexpr int kQHalf = kQBytes / 2;
-constexpr int kQOff = 0, kKOff = 2 * kQBytes, kVOff = kKOff + kKStages * kTileBytes;
+constexpr int kHalf = kTileBytes / 2;  // one 64-wide block of a tile: 128 rows of 128 bytes
+constexpr int kQOff = 0, kKOff = 2 * kTileBytes, kVOff = kKOff + kKStages * kTileBytes;
 constexpr int kBarOff = kVOff + kVStages * kTileBytes;
-constexpr int kBarBytes = 8 * (2 * kKStages + 2 * kVStages + 4 + 4 + 2 + 2 + 2 + 2 * kRawStages + 2);
-constexpr int kRawOff = kBarOff + 384, kRawBytes = 34176;  // packed parts: at most 18,432 bytes each
+constexpr int kBarBytes = 8 * (2 * kKStages + 2 * kVStages + 4 * 2 + 2 * kRawStages + 1);
+constexpr int kRawOff = kBarOff + 256, kRawBytes = 34304;  // packed parts: at most 18,432 bytes each
 constexpr int kSmemBytes = kRawOff + kRawBytes + 1024;     // + alignment of the base to 1024
 static_assert(kBarBytes <= kRawOff - kBarOff && kSmemBytes + 128 <= 227 * 1024, "shared memory of one CTA");
-constexpr int kTmemS = 0, kTmemO = 256;  // columns of slot 0 (scores: two buffers); slot 1 is 128 further
-constexpr float kLazy = 8.f, kOffset = 6.f;
+constexpr int kTmemS = 0, kTmemO = 256;           // columns of slot 0; slot 1 is 128 further
+constexpr float kOffset = 6.f, kMost = 16384.f;
 constexpr long long kWaitCycles = 4000000000LL;
 
 // ------------------------------------------------------------- PTX helpers
@@ -222,14 +218,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // Instruction descriptor: fp32 accumulator, A and B f16 or bf16, B MN-major or
-// K-major, M = 128, N = n.
-__device__ __forceinline__ uint32_t inst_desc(bool bf16, bool b_mn, int n) {
+// K-major, N = M = 128.
+__device__ __forceinline__ uint32_t inst_desc(bool bf16, bool b_mn) {
   const uint32_t t = bf16 ? 1u : 0u;
-  return (1u << 4) | (t << 7) | (t << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+  return (1u << 4) | (t << 7) | (t << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(kTile >> 3) << 17) |
          ((uint32_t)(kRows >> 4) << 24);
 }
 
-// The chunk's keys and values as matrices [tokens][Hkv * D], boxes of 64
+// The chunk's keys and values as matrices [tokens][Hkv * D], boxes of 128
 // tokens x 64 channels with the 128-byte swizzle.
 struct alignas(64) ChunkMaps {
   CUtensorMap k, v;
@@ -368,7 +364,7 @@ __device__ __forceinline__ void zero_row(uint32_t row) {
 }
 
 struct Bars {  // shared-memory addresses of arrays of barriers
-  uint32_t k_full, k_empty, v_full, v_empty, s_full, p_ready, pv_done, o_done, q_ready, raw_full, raw_empty, drain;
+  uint32_t k_full, k_empty, v_full, v_empty, s_full, p_ready, o_done, q_ready, raw_full, raw_empty, drain;
 };
 
 // Packed parts. Warp 17 copies every 64-token part of the item's quantized
@@ -406,12 +402,12 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const uint8_t* src, uint3
 // One thread.
 __device__ bool copy_parts(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, volatile int* abort) {
   const LayerView& L = p.L;
-  const int parts = min(it.k1, it.nA) - it.k0;
+  const int tiles = min(it.k1, it.nA) - it.k0;
   const RawLayout raw(L);
   RawRing ring(raw.stages);
   const int G = L.group_k;
-  for (int u = 0; u < parts; ++u, ring.next()) {
-    const int pos = (it.a0 + it.k0 + u) * kTile;
+  for (int u = 0; u < 2 * tiles; ++u, ring.next()) {
+    const int pos = (it.a0 + it.k0) * kTile + 64 * u;
     if (u >= raw.stages && !mbar_wait(bar.raw_empty + 8 * ring.stage, ring.parity ^ 1u, abort)) {
       for (int v = u - raw.stages; v < u; ++v) mbar_drain(bar.raw_full + 8 * (v % raw.stages), (v / raw.stages) & 1);
       return false;
@@ -463,7 +459,7 @@ __device__ __forceinline__ void release_raw(const Bars& bar, const RawRing& ring
 template <int KB>
 __device__ bool produce_keys(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, int kt,
                              volatile int* abort) {
-  const int parts = min(it.k1, it.nA) - it.k0;
+  const int parts = 2 * (min(it.k1, it.nA) - it.k0);
   if (parts <= 0) return true;
   const LayerView& L = p.L;
   const bool axis0 = L.k_axis == 0, wide = L.group_k >= 64;
@@ -517,8 +513,8 @@ __device__ bool produce_keys(const ChunkParams& p, const Item& it, uint32_t smem
       }
     }
     if (axis0) release_raw(bar, ring);
-    if (!mbar_wait_warp(bar.k_empty + 8 * st, phase, abort)) return false;
-    const uint32_t row = dst + st * kTileBytes;
+    if (!(u & 1) && !mbar_wait_warp(bar.k_empty + 8 * st, phase, abort)) return false;
+    const uint32_t row = dst + st * kTileBytes + (u & 1) * kHalf;
     if (valid <= 0) {
       zero_row(row);
     } else if (axis0) {
@@ -553,12 +549,14 @@ __device__ bool produce_keys(const ChunkParams& p, const Item& it, uint32_t smem
       });
     }
     if (!axis0) release_raw(bar, ring);
-    fence_async_smem();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar.k_full + 8 * st);
-    if (++st == kKStages) {
-      st = 0;
-      phase ^= 1u;
+    if (u & 1) {
+      fence_async_smem();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(bar.k_full + 8 * st);
+      if (++st == kKStages) {
+        st = 0;
+        phase ^= 1u;
+      }
     }
   }
   return true;
@@ -581,7 +579,7 @@ __device__ __forceinline__ int value_token(int i, int kb, bool pair32) {
 template <int VB>
 __device__ bool produce_values(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, int vt,
                                volatile int* abort) {
-  const int parts = min(it.k1, it.nA) - it.k0;
+  const int parts = 2 * (min(it.k1, it.nA) - it.k0);
   if (parts <= 0) return true;
   const LayerView& L = p.L;
   const RawLayout raw(L);
@@ -625,8 +623,8 @@ __device__ bool produce_values(const ChunkParams& p, const Item& it, uint32_t sm
     // have to pass through it, and the product that frees a value stage is
     // issued after the next scores)
     release_raw(bar, ring);
-    if (!mbar_wait_warp(bar.v_empty + 8 * st, phase, abort)) return false;
-    const uint32_t row = dst + st * kTileBytes;
+    if (!(u & 1) && !mbar_wait_warp(bar.v_empty + 8 * st, phase, abort)) return false;
+    const uint32_t row = dst + st * kTileBytes + (u & 1) * (64 * 128);
     if (valid <= 0) {
       zero_row(row);
     } else {
@@ -635,12 +633,14 @@ __device__ bool produce_values(const ChunkParams& p, const Item& it, uint32_t sm
         z2 = z[pair >> 4];
       });
     }
-    fence_async_smem();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar.v_full + 8 * st);
-    if (++st == kVStages) {
-      st = 0;
-      phase ^= 1u;
+    if (u & 1) {
+      fence_async_smem();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(bar.v_full + 8 * st);
+      if (++st == kVStages) {
+        st = 0;
+        phase ^= 1u;
+      }
     }
   }
   return true;
@@ -744,7 +744,7 @@ __device__ __forceinline__ float load_query(const ChunkParams& p, const Item& it
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
       const uint4 v = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-      sts16(dst + (c >> 3) * kQHalf + (((c & 7) ^ (row & 7)) << 4), v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+      sts16(dst + (c >> 3) * kHalf + (((c & 7) ^ (row & 7)) << 4), v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
     }
     return fmaxf(scale, 1e-37f);  // never 0: a masked score is -inf times this
   }
@@ -777,7 +777,7 @@ __device__ __forceinline__ float load_query(const ChunkParams& p, const Item& it
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = pack2<false>(x[8 * c + 2 * j] * up, x[8 * c + 2 * j + 1] * up);
-    sts16(dst + (c >> 3) * kQHalf + (((c & 7) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+    sts16(dst + (c >> 3) * kHalf + (((c & 7) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
   }
   return fmaxf(scale * __uint_as_float((uint32_t)(127 - e) << 23), 1e-37f);
 }
@@ -841,7 +841,8 @@ struct RowState {
 };
 // Packed probabilities 2^(s cs + bias) of 32 columns, added to sum.
 template <bool BF16>
-__device__ __forceinline__ void probabilities(const uint32_t* s, float cs, float bias, uint32_t* w, uint64_t& sum) {
+__device__ __forceinline__ void probabilities(const uint32_t* s, float cs, float bias, uint32_t* w,
+                                              uint64_t (&sum)[4]) {
   const uint64_t cs2 = pair_of(cs, cs), b2 = pair_of(bias, bias);
 #pragma unroll
   for (int c = 0; c < 16; ++c) {
@@ -849,64 +850,73 @@ __device__ __forceinline__ void probabilities(const uint32_t* s, float cs, float
     unpair(fma2(pair_of(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), cs2, b2), a, b);
     a = ex2(a);
     b = ex2(b);
-    sum = add2(sum, pair_of(a, b));
+    sum[c & 3] = add2(sum[c & 3], pair_of(a, b));
     w[c] = pack2<BF16>(a, b);
   }
 }
-// The probabilities of one tile (scores in s), as packed pairs over its first
-// 32 columns. They go by the m so far, so that nothing waits for the tile's
-// maximum; where that turns out to pass m by more than kLazy (always on a row's
-// first tile), m is raised, O rescaled (once the slot's product before this one,
-// at the parity given, is complete) and the tile computed again. false when the
-// item was aborted.
+// Half a tile (64 columns, scores in s). The probabilities go by the m so far.
+// Their sum tells whether that was good enough: below 2^kMost none of them
+// passes fp16's range. Else (always on a row's first tile, hardly ever later) m
+// is raised to the maximum, what was written is rescaled and the half is
+// computed again. Packed pairs go over the columns 32h .. of the scores already
+// read.
 template <bool BF16>
-__device__ __forceinline__ bool softmax_row(const uint32_t (&s)[64], float cs, RowState& st, uint32_t tm_s,
-                                            uint32_t tm_o, bool have_o, uint32_t pv_done, uint32_t parity,
-                                            volatile int* abort) {
+__device__ __forceinline__ void softmax_half(const uint32_t (&s)[64], int h, float cs, RowState& st, uint32_t tm_s,
+                                             uint32_t tm_o, bool have_o) {
   uint32_t w[32];
-  uint64_t sum = 0;
+  uint64_t sum[4] = {0, 0, 0, 0};
+  float a, b;
   probabilities<BF16>(s, cs, kOffset - st.m, w, sum);
   probabilities<BF16>(s + 32, cs, kOffset - st.m, w + 16, sum);
-  float mx[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(s[e]);
-#pragma unroll
-  for (int c = 4; c < 60; c += 8)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
-#pragma unroll
-  for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[60 + e]));
-  const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
-  const bool grow = top > st.m + kLazy;
+  unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+  float l = a + b;
   // (a row that has seen nothing yet computed 2^(-inf + inf): again, as zeros)
-  if (__any_sync(0xffffffffu, grow || st.m == -INFINITY)) {
-    const float m = grow ? ceilf(top) : st.m;
-    const float a = grow ? ex2(st.m - m) : 1.f;  // a power of two; 0 while m = -inf
+  if (__any_sync(0xffffffffu, !(l < kMost) || st.m == -INFINITY)) {
+    float top = __uint_as_float(s[0]);
+#pragma unroll
+    for (int c = 1; c < 63; c += 2) top = max3(top, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+    top = fmaxf(top, __uint_as_float(s[63])) * cs;
+    const float m = top > st.m ? ceilf(top) : st.m;
+    const float f = m > st.m ? ex2(st.m - m) : 1.f;  // a power of two; 0 while m = -inf
     st.m = m;
-    st.l *= a;
-    sum = 0;
+    st.l *= f;
     const float bias = m == -INFINITY ? 0.f : kOffset - m;
+    sum[0] = sum[1] = sum[2] = sum[3] = 0;
     probabilities<BF16>(s, cs, bias, w, sum);
     probabilities<BF16>(s + 32, cs, bias, w + 16, sum);
+    unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+    l = a + b;
+    // the slot's previous product is complete (its scores' barrier completed
+    // after it), and so O is at rest; the tile's own probabilities so far too
+    tmem_wait_st();
     if (have_o) {
-      if (!mbar_wait_warp(pv_done, parity, abort)) return false;
-      tc_after();
 #pragma unroll 1
       for (int c = 0; c < kD; c += 16) {
         uint32_t o[16];
         tmem_ld16(tm_o + c, o);
         tmem_wait_ld16(o);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
         tmem_st16(tm_o + c, o);
       }
     }
+#pragma unroll 1
+    for (int c = 0; c < 2 * h; ++c) {
+      uint32_t o[16];
+      tmem_ld16(tm_s + 16 * c, o);
+      tmem_wait_ld16(o);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float2 x;
+        if constexpr (BF16) x = make_float2(__uint_as_float(o[e] << 16), __uint_as_float(o[e] & 0xffff0000u));
+        else x = __half22float2(half2_of(o[e]));
+        o[e] = pack2<BF16>(x.x * f, x.y * f);
+      }
+      tmem_st16(tm_s + 16 * c, o);
+    }
   }
-  tmem_st32(tm_s, w);
-  float a, b;
-  unpair(sum, a, b);
-  st.l += a + b;
-  return true;
+  tmem_st32(tm_s + 32 * h, w);
+  st.l += l;
 }
 // Scores whose bit is clear become -inf.
 __device__ __forceinline__ void mask_chunk(uint32_t* s, uint32_t bits) {
@@ -922,8 +932,8 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
   const int t = min(r, it.rows - 1) / it.ngr;  // the row's new token
   const bool bf16 = L.kv_dtype == KVQ_BF16;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-  const uint32_t tm_s = tmem + lanes + kTmemS + w * 2 * kTile, tm_o = tmem + lanes + kTmemO + w * kD;
-  const uint32_t qtile = smem + kQOff + w * kQBytes;
+  const uint32_t tm_s = tmem + lanes + kTmemS + w * kTile, tm_o = tmem + lanes + kTmemO + w * kD;
+  const uint32_t qtile = smem + kQOff + w * kTileBytes;
   const int n = it.slot_tiles(w);
   RowState st;
   float cs = 0.f;
@@ -961,32 +971,32 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
     // what the tile needs is worked out before the wait for its scores
     const int at = in_a ? (it.a0 + k) * kTile : it.tile_b(k) * kTile;  // its first position or entry
     const bool masked = in_a ? at + kTile > it.q || at <= last_lo_a : at + kTile - 1 > first_hi || at <= last_lo_b;
-    const uint32_t tm = tm_s + (j & 1) * kTile, buf = 16 * w + 8 * (j & 1);  // the tile's score buffer
-    if (!mbar_wait_warp(bar.s_full + buf, (j >> 1) & 1, abort)) return false;
+    if (!mbar_wait_warp(bar.s_full + 8 * w, j & 1, abort)) return false;
     tc_after();
-    uint32_t s[kTile];
-    tmem_ld32(tm, s);
-    tmem_ld32(tm + 32, s + 32);
-    tmem_wait_ld(s);
-    tmem_wait_ld(s + 32);
-    if (masked) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t s[64];
+      tmem_ld32(tm_s + 64 * h, s);
+      tmem_ld32(tm_s + 64 * h + 32, s + 32);
+      tmem_wait_ld(s);
+      tmem_wait_ld(s + 32);
+      if (masked) {
 #pragma unroll
-      for (int c = 0; c < kTile; c += 32) {
-        if (in_a)
-          mask_chunk(s + c, shuffle_bits(bit_range(lo_a + 1 - at - c, it.q - at - c), per));
-        else
-          mask_chunk(s + c, bit_range(lo_b + 1 - at - c, hi_b + 1 - at - c) |
-                                bit_range(0, min(it.first_e, hi_b + 1) - at - c));
+        for (int e = 0; e < 64; e += 32) {
+          const int c = at + 64 * h + e;
+          if (in_a)
+            mask_chunk(s + e, shuffle_bits(bit_range(lo_a + 1 - c, it.q - c), per));
+          else
+            mask_chunk(s + e, bit_range(lo_b + 1 - c, hi_b + 1 - c) | bit_range(0 - c, min(it.first_e, hi_b + 1) - c));
+        }
       }
+      if (in_a || !bf16) softmax_half<false>(s, h, cs, st, tm_s, tm_o, j > 0);
+      else softmax_half<true>(s, h, cs, st, tm_s, tm_o, j > 0);
     }
-    const bool ok = in_a || !bf16
-                        ? softmax_row<false>(s, cs, st, tm, tm_o, j > 0, bar.pv_done + 8 * w, (j - 1) & 1, abort)
-                        : softmax_row<true>(s, cs, st, tm, tm_o, j > 0, bar.pv_done + 8 * w, (j - 1) & 1, abort);
-    if (!ok) return false;
     tmem_wait_st();
     tc_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar.p_ready + buf);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar.p_ready + 8 * w);
   }
   // ---- the row's output or part
   const bool there = r < it.rows;
@@ -1046,91 +1056,89 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride, version, swizzle
 constexpr uint32_t kDescK = 1u << 16, kDescMn = (uint32_t)(kHalf >> 4) << 16;  // leading offset
 // The eight k-steps of one slot's scores (MN: expanded keys, else exact ones)
-// and the four of its product with the values.
+// and of its product with the values.
 template <bool MN>
 __device__ __forceinline__ void issue_scores(uint32_t d, uint32_t q_lo, uint32_t k_lo, uint32_t id) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int qs = ((e >> 2) * kQHalf + (e & 3) * 32) >> 4;
-    const int ks = MN ? (e * 2048) >> 4 : ((e >> 2) * kHalf + (e & 3) * 32) >> 4;
-    mma_ss(d, desc_of(q_lo + qs, kDescHi), desc_of(k_lo + ks, kDescHi), id, e > 0);
+    constexpr int kStep = 2048 >> 4;
+    const int step = ((e >> 2) * kHalf + (e & 3) * 32) >> 4;
+    mma_ss(d, desc_of(q_lo + step, kDescHi), desc_of(k_lo + (MN ? e * kStep : step), kDescHi), id, e > 0);
   }
 }
 __device__ __forceinline__ void issue_values(uint32_t d, uint32_t p, uint32_t v_lo, uint32_t id, bool acc) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) mma_ts(d, p + 8 * e, desc_of(v_lo + e * (2048 >> 4), kDescHi), id, acc || e > 0);
+  for (int e = 0; e < 8; ++e) mma_ts(d, p + 8 * e, desc_of(v_lo + e * (2048 >> 4), kDescHi), id, acc || e > 0);
 }
 
-// One warp per slot issues its products (by one elected lane; the warp walks
-// the loop together, so that descriptors are warp-uniform values). Per phase:
-// S of the first two tiles, then P V of tile j and S of tile j + 2: the scores
-// of tile j + 2 are queued behind the product of tile j (which reads the P they
-// overwrite), while those of tile j + 1 are ready before the softmax of tile j
-// ends, so that the softmax warps do not wait for the tensor cores. Phase B
-// starts when phase A's products are issued: the queries are rewritten in
-// between. (A step costs its warp about 1000 cycles of waits, commits and
-// issue, as long as the tensor cores work on it: one warp for both slots was
-// what bounded the kernel.)
-__device__ bool issue_products(const ChunkParams& p, const Item& it, int w, uint32_t smem, uint32_t tmem,
-                               const Bars& bar, volatile int* abort) {
+// One warp issues every product of the item (by one elected lane; the warp
+// walks the loop together, so that descriptors are warp-uniform values), in the
+// order S(0), S(1), then
+// P V of step v and S of step v + 2: a slot's next scores are queued behind
+// its own product (which reads the P they overwrite) while the other slot's
+// softmax runs. The tensor cores idle while this thread does anything else, so
+// a step is kept short: what it needs is counted, not worked out. (One warp per
+// slot lets the slots fall into step with each other: 12% slower.)
+__device__ bool issue_products(const ChunkParams& p, const Item& it, uint32_t smem, uint32_t tmem, const Bars& bar,
+                               volatile int* abort) {
+  const int steps = it.steps();
   const bool leader = elect_one();
-  const bool bf16 = p.L.kv_dtype == KVQ_BF16;
-  const uint32_t q_lo = ((smem + kQOff + w * kQBytes) >> 4) | kDescK;
+  const bool bf16 = p.L.kv_dtype == KVQ_BF16, both = it.both;
+  const uint32_t q_lo = ((smem + kQOff) >> 4) | kDescK;
   const uint32_t k_base = (smem + kKOff) >> 4, v_lo = ((smem + kVOff) >> 4) | kDescMn;
-  const uint32_t sd = tmem + kTmemS + 2 * w * kTile, od = tmem + kTmemO + w * kD;  // scores (and P), O
+  const uint32_t id_a = inst_desc(false, true), id_bk = inst_desc(bf16, false), id_bv = inst_desc(bf16, true);
   constexpr uint32_t kTileLo = kTileBytes >> 4;
-  static_assert(kKStages == 4 && kVStages == 4, "stages are counted in two bits");
-  const int sh = it.both ? 0 : 1, n0 = it.both ? 0 : w;  // the slot's tile j: tile n0 + (j << sh) of the item
-  const int first_b = min(it.k1, max(it.k0, it.nA)) - it.k0;  // tiles of the item before phase B
-  const int tiles_a = max(0, (first_b - n0 + sh) >> sh);      // the slot's
-  const uint32_t k_empty = bar.k_empty, v_empty = bar.v_empty, s_full = bar.s_full + 16 * w;
-#pragma unroll 1
-  for (int ph = 0; ph < 2; ++ph) {
-    const int j0 = ph ? tiles_a : 0, j1 = ph ? it.slot_tiles(w) : tiles_a;
-    const uint32_t id_s = ph ? inst_desc(bf16, false, kTile) : inst_desc(false, true, kTile);
-    const uint32_t id_v = ph ? inst_desc(bf16, true, kD) : inst_desc(false, true, kD);
-    auto scores = [&](int j) {
-      const int b = j & 1, st = (n0 + (j << sh)) & 3;
-      const uint32_t d = sd + b * kTile, lo = k_base + st * kTileLo;
-      if (ph == 0) {
-        if (leader) issue_scores<true>(d, q_lo, lo | kDescMn, id_s);
-      } else {
-        if (leader) issue_scores<false>(d, q_lo, lo | kDescK, id_s);
-      }
-      if (leader) {
-        tc_commit(s_full + 8 * b);
-        tc_commit(k_empty + 8 * st);
-      }
-      __syncwarp();
-    };
-    auto wait_keys = [&](int j) {
-      const int n = n0 + (j << sh);
-      return mbar_wait_warp(bar.k_full + 8 * (n & 3), (n >> 2) & 1, abort);
-    };
-    // the slot's query of this phase: its second one if it has tiles of phase A
-    if (j0 < j1 && !mbar_wait_warp(bar.q_ready + 8 * w, ph && tiles_a > 0 ? 1 : 0, abort)) return false;
-    for (int j = j0; j < j0 + 2 && j < j1; ++j) {
-      if (!wait_keys(j)) return false;
-      tc_after();
-      scores(j);
+  static_assert(kKStages == 2 && kVStages == 2, "stages are counted in one bit");
+  const int first_b = it.nA - it.k0;  // tiles of the item before phase B
+  // tile n of the item (counted from k0) sits in stage n % 2, in phase n / 2
+  auto scores = [&](int w, int n) {
+    const uint32_t lo = k_base + (n & 1) * kTileLo, d = tmem + kTmemS + w * kTile, q = q_lo + w * kTileLo;
+    if (n < first_b) {
+      if (leader) issue_scores<true>(d, q, lo | kDescMn, id_a);
+    } else {
+      if (leader) issue_scores<false>(d, q, lo | kDescK, id_bk);
     }
+    if (leader) tc_commit(bar.s_full + 8 * w);
+    if (leader && (!both || w == 1)) tc_commit(bar.k_empty + 8 * (n & 1));
+    __syncwarp();
+  };
+  for (int v = 0; v < 2 && v < steps; ++v) {
+    const int n = both ? 0 : v;
+    if (!mbar_wait_warp(bar.q_ready + 8 * v, 0, abort)) return false;
+    if (!mbar_wait_warp(bar.k_full + 8 * (n & 1), 0, abort)) return false;
+    tc_after();
+    scores(v, n);
+  }
+  int n = 0;  // tile of step v; the slot's next tile is n + ahead
+  const int ahead = both ? 1 : 2;
 #pragma unroll 1
-    for (int j = j0; j < j1; ++j) {
-      const int b = j & 1, n = n0 + (j << sh), st = n & 3;
-      const bool more = j + 2 < j1;
-      if (!mbar_wait_warp(bar.v_full + 8 * st, (n >> 2) & 1, abort)) return false;
-      if (more && !wait_keys(j + 2)) return false;
-      if (!mbar_wait_warp(bar.p_ready + 16 * w + 8 * b, (j >> 1) & 1, abort)) return false;
-      tc_after();
-      if (leader) {
-        issue_values(od, sd + b * kTile, v_lo + st * kTileLo, id_v, j > 0);
-        tc_commit(bar.pv_done + 8 * w);
-        if (j == j1 - 1) tc_commit(bar.o_done + 8 * w);  // the slot's last product of the phase
-        tc_commit(v_empty + 8 * st);
-      }
-      __syncwarp();
-      if (more) scores(j + 2);
+  for (int v = 0; v < steps; ++v) {
+    const int w = v & 1, next = n + ahead;
+    const bool more = v + 2 < steps;
+    // a slot that enters phase B rewrites its query only after this product
+    const bool enter_b = more && next >= first_b && n < first_b;
+    if (!both || w == 0) {
+      if (!mbar_wait_warp(bar.v_full + 8 * (n & 1), (n >> 1) & 1, abort)) return false;
+      if (more && !mbar_wait_warp(bar.k_full + 8 * (next & 1), (next >> 1) & 1, abort)) return false;
     }
+    if (!mbar_wait_warp(bar.p_ready + 8 * w, (v >> 1) & 1, abort)) return false;
+    tc_after();
+    const uint32_t od = tmem + kTmemO + w * kD, op = tmem + kTmemS + w * kTile, ov = v_lo + (n & 1) * kTileLo;
+    const uint32_t id = n < first_b ? id_a : id_bv;
+    if (leader) {
+      issue_values(od, op, ov, id, v > 1);
+      if (!more || enter_b) tc_commit(bar.o_done + 8 * w);  // the slot's last product of the phase
+    }
+    if (leader && (!both || w == 1)) tc_commit(bar.v_empty + 8 * (n & 1));
+    __syncwarp();
+    if (more) {
+      if (enter_b) {
+        if (!mbar_wait_warp(bar.q_ready + 8 * w, 1, abort)) return false;
+        tc_after();
+      }
+      scores(w, next);
+    }
+    n += both ? w : 1;
   }
   return true;
 }
@@ -1149,9 +1157,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
     bar.k_empty = at, at += 8 * kKStages;
     bar.v_full = at, at += 8 * kVStages;
     bar.v_empty = at, at += 8 * kVStages;
-    bar.s_full = at, at += 32;
-    bar.p_ready = at, at += 32;
-    bar.pv_done = at, at += 16;
+    bar.s_full = at, at += 16;
+    bar.p_ready = at, at += 16;
     bar.o_done = at, at += 16;
     bar.q_ready = at, at += 16;
     bar.raw_full = at, at += 8 * kRawStages;
@@ -1162,18 +1169,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(bar.k_full + 8 * i, kProducers / 32);
-      mbar_init(bar.k_empty + 8 * i, it.both ? 2 : 1);
+      mbar_init(bar.k_empty + 8 * i, 1);
     }
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(bar.v_full + 8 * i, kProducers / 32);
-      mbar_init(bar.v_empty + 8 * i, it.both ? 2 : 1);
-    }
-    for (int i = 0; i < 4; ++i) {  // [slot][buffer]
-      mbar_init(bar.s_full + 8 * i, 1);
-      mbar_init(bar.p_ready + 8 * i, 4);
+      mbar_init(bar.v_empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar.pv_done + 8 * i, 1);
+      mbar_init(bar.s_full + 8 * i, 1);
+      mbar_init(bar.p_ready + 8 * i, 4);
       mbar_init(bar.o_done + 8 * i, 1);
       mbar_init(bar.q_ready + 8 * i, 4);
     }
@@ -1182,7 +1186,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
       mbar_init(bar.raw_empty + 8 * i, 2 * kProducers / 32);
     }
     mbar_init(bar.drain, 1);
-    mbar_init(bar.drain + 8, 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1218,12 +1221,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
                                     abort);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    const int w = (warp >> 1) & 1;
-    if (!(warp & 1) && !issue_products(p, it, w, smem, tmem, bar, abort)) {
+    if (warp == 16 && !issue_products(p, it, smem, tmem, bar, abort)) {
       // let the products in flight finish before the tensor memory goes
-      if (elect_one()) tc_commit(bar.drain + 8 * w);
+      if (elect_one()) tc_commit(bar.drain);
       __syncwarp();
-      mbar_drain(bar.drain + 8 * w, 0);
+      mbar_drain(bar.drain, 0);
       __syncwarp();
     }
     if (warp == 17 && (threadIdx.x & 31) == 0) (void)copy_parts(p, it, smem, bar, abort);
