@@ -71,23 +71,17 @@ __global__ void __launch_bounds__(32 * kWarps) chunk_simple_kernel(ChunkParams p
   const LayerView& L = p.L;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.x;
-  int lo = 0, hi = p.nseq - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.item0[mid] <= item) lo = mid;
-    else hi = mid - 1;
-  }
-  const int i = lo, b = p.seq[i];
-  const int h = (item - p.item0[i]) % L.num_kv_heads, rt = (item - p.item0[i]) / L.num_kv_heads;
+  const int i = p.entry_of_item(item), b = p.e[i].seq;
+  const int h = (item - p.e[i].item0) % L.num_kv_heads, rt = (item - p.e[i].item0) / L.num_kv_heads;
   const int ngr = p.num_q_heads / L.num_kv_heads;
-  const int rows = p.t_new[i] * ngr, r0 = rt * kChunkRows;  // row r: token r / ngr, head h * ngr + r % ngr
-  const int s = p.s[i], len = s + p.q_len[i] + p.n_len[i];
+  const int rows = p.e[i].t * ngr, r0 = rt * kChunkRows;  // row r: token r / ngr, head h * ngr + r % ngr
+  const int s = p.e[i].s, len = s + p.e[i].q + p.e[i].n;
   const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q);
   for (int e = threadIdx.x; e < kChunkRows * kHeadDim; e += blockDim.x) {
     const int r = r0 + e / kHeadDim;
     float x = 0.f;
     if (r < rows) {
-      const int64_t row = (int64_t)(p.in_off[i] + r / ngr) * p.num_q_heads + h * ngr + r % ngr;
+      const int64_t row = (int64_t)(p.e[i].off + r / ngr) * p.num_q_heads + h * ngr + r % ngr;
       x = load_kv(q, row * kHeadDim + e % kHeadDim, L.kv_dtype) * p.scale_log2;
     }
     sq[e / kHeadDim][e % kHeadDim] = x;
@@ -121,10 +115,10 @@ __global__ void __launch_bounds__(32 * kWarps) chunk_simple_kernel(ChunkParams p
           y[e] = load_kv(L.sink_v, row + e, L.kv_dtype);
         }
       } else if (c < len) {
-        cached_token<true>(L, b, h, c - s, p.q_len[i], lane, x);
-        cached_token<false>(L, b, h, c - s, p.qv_len[i], lane, y);
+        cached_token<true>(L, b, h, c - s, p.e[i].q, lane, x);
+        cached_token<false>(L, b, h, c - s, p.e[i].qv, lane, y);
       } else if (c < end) {
-        const int64_t row = ((int64_t)(p.in_off[i] + c - len) * L.num_kv_heads + h) * kHeadDim + 4 * lane;
+        const int64_t row = ((int64_t)(p.e[i].off + c - len) * L.num_kv_heads + h) * kHeadDim + 4 * lane;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           x[e] = load_kv(p.k, row + e, L.kv_dtype);
@@ -176,7 +170,7 @@ __global__ void __launch_bounds__(32 * kWarps) chunk_simple_kernel(ChunkParams p
   for (int e = 0; e < kRowsPerWarp; ++e) {
     const int r = r0 + warp * kRowsPerWarp + e;
     if (r >= rows) break;
-    const int64_t at = ((int64_t)(p.in_off[i] + r / ngr) * p.num_q_heads + h * ngr + r % ngr) * kHeadDim + 4 * lane;
+    const int64_t at = ((int64_t)(p.e[i].off + r / ngr) * p.num_q_heads + h * ngr + r % ngr) * kHeadDim + 4 * lane;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
       const float x = __fdiv_rn(o[e][d], l[e]);  // every row sees its own token

@@ -7,45 +7,69 @@
 
 namespace kvq {
 
-// One launch. The tables hold the sequences that have new tokens, in launch
-// order (the host puts the longest work first); entry i is sequence seq[i].
-// Positions: cached token c of a sequence is sink c (c < s), then position
-// c - s after the sinks: a quantized token below q (keys) / qv (values), else
-// a ring token. New token t is the sequence's token len + t, len = s + q + n.
-// Query token t sees token c when c <= len + t and, with a window, when also
-// c > len + t - window or c < sink_tokens.
+// A sequence with new tokens, in launch order (the host puts the longest work
+// first). Positions: cached token c of a sequence is sink c (c < s), then
+// position c - s after the sinks: a quantized token below q (keys) / qv
+// (values), else a ring token. New token t is the sequence's token len + t,
+// len = s + q + n. Query token t sees token c when c <= len + t and, with a
+// window, when also c > len + t - window or c < sink_tokens. The fields of an
+// entry lie together: a CTA reads them once, from a cold constant cache.
+struct ChunkEntry {
+  int32_t item0;  // first work item
+  int32_t seq;
+  int32_t s, q, qv, n;  // host mirror of the lengths
+  int32_t t;      // new tokens
+  int32_t off;    // first row of the sequence in k, v, q and out
+  // Tensor-core kernel: how the sequence's units (KV head, tile of query rows)
+  // are cut. splits > 0: so many ranges of the tokens, both slots of a CTA on
+  // every tile (256 rows); splits < 0: -splits ranges, the slots on alternate
+  // tiles (at most 128 rows). A row of several parts leaves part j at record
+  // part0 + (h * rows + r) * parts + j of ws_o / ws_ml, and the merge kernel
+  // joins the rows merge0 .. of all entries (entries of one part take none).
+  int32_t splits, part0, merge0;
+  int32_t pad;
+};
+
+// One launch.
 struct ChunkParams {
   LayerView L;
   const void* k;        // [tokens][Hkv][D] kv dtype, the chunk's keys
   const void* v;
   const void* q;        // [tokens][Hq][D] kv dtype
   void* out;            // [tokens][Hq][D] out dtype
+  float* ws_o;          // [records][D]
+  float2* ws_ml;        // [records]: (maximum in log2 units, sum)
+  int32_t* err;
   float scale_log2;     // softmax scale * log2(e)
   int32_t out_dtype;
   int32_t num_q_heads;
   int32_t window;       // 0: none
   int32_t sink_tokens;  // S of the cache: tokens that stay visible outside the window
   int32_t tokens;       // rows of k and v
-  int32_t nseq;         // entries of the tables
+  int32_t nseq;         // entries
   int32_t items;        // work items of all entries
-  int32_t seq[KVQ_MAX_BATCH];
-  int32_t s[KVQ_MAX_BATCH], q_len[KVQ_MAX_BATCH], qv_len[KVQ_MAX_BATCH], n_len[KVQ_MAX_BATCH];  // host mirror
-  int32_t t_new[KVQ_MAX_BATCH];   // new tokens
-  int32_t in_off[KVQ_MAX_BATCH];  // first row of the sequence in k, v, q and out
-  int32_t item0[KVQ_MAX_BATCH];   // first work item
-  // Tensor-core kernel: how a sequence's units (KV head, tile of query rows)
-  // are cut. splits > 0: so many ranges of the tokens, both slots of a CTA on
-  // every tile (256 rows); splits < 0: -splits ranges, the slots on alternate
-  // tiles (at most 128 rows). A row of several parts leaves part j at record
-  // part0 + (h * rows + r) * parts + j of ws_o / ws_ml, and the merge kernel
-  // joins the rows merge0 .. of all entries (entries of one part take none).
-  float* ws_o;          // [records][D]
-  float2* ws_ml;        // [records]: (maximum in log2 units, sum)
-  int32_t* err;
   int32_t merge_rows;
-  int32_t splits[KVQ_MAX_BATCH];
-  int32_t merge0[KVQ_MAX_BATCH];
-  int32_t part0[KVQ_MAX_BATCH];
+  ChunkEntry e[KVQ_MAX_BATCH];
+
+  // The entry that work item (merge row) x belongs to.
+  __device__ __forceinline__ int entry_of_item(int x) const {
+    int lo = 0, hi = nseq - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (e[mid].item0 <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  }
+  __device__ __forceinline__ int entry_of_merge(int x) const {
+    int lo = 0, hi = nseq - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (e[mid].merge0 <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  }
 };
 // Parts of each row of an entry with these splits.
 __host__ __device__ inline int chunk_parts(int splits) { return splits < 0 ? -2 * splits : splits; }

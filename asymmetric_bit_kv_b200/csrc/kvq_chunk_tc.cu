@@ -249,36 +249,30 @@ struct Item {
     return b_sink ? (j == 0 ? 0 : b0 + j - 1) : b0 + j;
   }
   __device__ __forceinline__ int steps() const { return both ? 2 * (k1 - k0) : k1 - k0; }
-  // tiles of slot w, and its j-th one
+  // tiles of slot w
   __device__ __forceinline__ int slot_tiles(int w) const { return both ? k1 - k0 : (k1 - k0 + 1 - w) / 2; }
-  __device__ __forceinline__ int slot_tile(int w, int j) const { return both ? k0 + j : k0 + 2 * j + w; }
 };
 
 __device__ __forceinline__ Item find_item(const ChunkParams& p, int idx) {
   Item it;
-  int lo = 0, hi = p.nseq - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.item0[mid] <= idx) lo = mid;
-    else hi = mid - 1;
-  }
+  const int lo = p.entry_of_item(idx);
   const int hkv = p.L.num_kv_heads;
   it.i = lo;
-  it.b = p.seq[lo];
+  it.b = p.e[lo].seq;
   it.ngr = p.num_q_heads / hkv;
-  it.rows = p.t_new[lo] * it.ngr;
-  it.both = p.splits[lo] > 0;
-  const int ns = abs(p.splits[lo]), tiles = (it.rows + 2 * kRows - 1) / (2 * kRows);
-  int x = idx - p.item0[lo];
+  it.rows = p.e[lo].t * it.ngr;
+  it.both = p.e[lo].splits > 0;
+  const int ns = abs(p.e[lo].splits), tiles = (it.rows + 2 * kRows - 1) / (2 * kRows);
+  int x = idx - p.e[lo].item0;
   const int sp = x % ns;
   x /= ns;
   it.h = x % hkv;
   it.r0 = (tiles - 1 - x / hkv) * 2 * kRows;  // the rows that see most first
   it.t0 = it.r0 / it.ngr;
   it.t1 = (min(it.r0 + 2 * kRows, it.rows) - 1) / it.ngr;
-  it.s = p.s[lo];
-  it.q = p.q_len[lo];
-  it.n = p.n_len[lo];
+  it.s = p.e[lo].s;
+  it.q = p.e[lo].q;
+  it.n = p.e[lo].n;
   const int after = it.n + it.t0 - p.window + 1;  // first visible entry past the quantized positions, if >= 0
   const int low_a = p.window > 0 ? max(0, it.q + after) : 0;
   it.a0 = low_a / kTile;
@@ -291,7 +285,7 @@ __device__ __forceinline__ Item find_item(const ChunkParams& p, int idx) {
   const int64_t total = it.nA + it.nB;
   it.k0 = (int)(total * sp / ns);
   it.k1 = (int)(total * (sp + 1) / ns);
-  it.parts = chunk_parts(p.splits[lo]);
+  it.parts = chunk_parts(p.e[lo].splits);
   it.part = it.both ? sp : 2 * sp;
   return it;
 }
@@ -659,7 +653,7 @@ __device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t til
   const int ch = kt & 15;
   const uint4* sink_p = reinterpret_cast<const uint4*>(sink) + unit * KVQ_MAX_SINKS * 16 + ch;
   const uint4* ring_p = reinterpret_cast<const uint4*>(ring) + unit * L.residual * 16 + ch;
-  const uint4* new_p = reinterpret_cast<const uint4*>(fresh) + ((int64_t)p.in_off[it.i] * L.num_kv_heads + it.h) * 16 + ch;
+  const uint4* new_p = reinterpret_cast<const uint4*>(fresh) + ((int64_t)p.e[it.i].off * L.num_kv_heads + it.h) * 16 + ch;
   const int64_t stride = (int64_t)L.num_kv_heads * 16;
   const int held = it.s + it.n, last = held + it.t1;
   const int slot0 = it.q % L.residual;  // ring slot of the first ring token
@@ -670,7 +664,7 @@ __device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t til
       return false;
     }
     const uint32_t dst = tiles + st * kTileBytes, bar = full + 8 * st;
-    if (e0 >= held && e0 - held + kTile <= p.t_new[it.i]) {
+    if (e0 >= held && e0 - held + kTile <= p.e[it.i].t) {
       if ((kt & 31) == 0) {
         if (kt == 0) {
           asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(kTileBytes) : "memory");
@@ -679,7 +673,7 @@ __device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t til
             asm volatile(
                 "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
                     dst + half * kHalf),
-                "l"(map), "r"(it.h * kD + 64 * half), "r"(p.in_off[it.i] + e0 - held), "r"(bar)
+                "l"(map), "r"(it.h * kD + 64 * half), "r"(p.e[it.i].off + e0 - held), "r"(bar)
                 : "memory");
         } else {
           mbar_arrive(bar);
@@ -735,7 +729,7 @@ __device__ __forceinline__ float load_query(const ChunkParams& p, const Item& it
                                             bool phase_a) {
   const bool there = r < it.rows;
   const bool bf16 = p.L.kv_dtype == KVQ_BF16;
-  const int64_t at = (int64_t)(p.in_off[it.i] + r / it.ngr) * p.num_q_heads + it.h * it.ngr + r % it.ngr;
+  const int64_t at = (int64_t)(p.e[it.i].off + r / it.ngr) * p.num_q_heads + it.h * it.ngr + r % it.ngr;
   const uint4* src = reinterpret_cast<const uint4*>(p.q) + at * 16;
   const uint32_t dst = tile + row * 128;
   const float scale = fabsf(p.scale_log2);
@@ -936,7 +930,6 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
   const uint32_t qtile = smem + kQOff + w * kTileBytes;
   const int n = it.slot_tiles(w);
   RowState st;
-  float cs = 0.f;
   const int per = 32 / L.k_bits;  // key codes per word
   const int hi_b = it.s + it.n + t;                        // phase B: the row's own entry
   const int lo_b = p.window > 0 ? hi_b - p.window : -1;     // entries up to this are hidden
@@ -944,66 +937,81 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
   // tile-uniform: does any row of the item hide something of a tile?
   const int first_hi = it.s + it.n + it.t0, last_lo_b = p.window > 0 ? it.s + it.n + it.t1 - p.window : -1;
   const int last_lo_a = p.window > 0 ? it.q + it.n + it.t1 - p.window : -1;
+  const uint32_t s_full = bar.s_full + 8 * w, p_ready = bar.p_ready + 8 * w;
+  const int step = it.both ? 1 : 2, k_first = it.k0 + (it.both ? 0 : w);  // the slot's tiles: k_first, + step, ...
+  const int tiles_a = min(n, max(0, (it.nA - k_first + step - 1) / step));
+  bool have_o = false;
+  uint32_t parity = 0;
 #pragma unroll 1
-  for (int j = 0; j < n; ++j) {
-    const int k = it.slot_tile(w, j);
-    const bool in_a = k < it.nA;
-    const bool enter_b = !in_a && (j == 0 || it.slot_tile(w, j - 1) < it.nA);
-    if (j == 0 || enter_b) {
-      if (j > 0) {  // every product of phase A must be in O, and have read Q
-        if (!mbar_wait_warp(bar.o_done + 8 * w, 0, abort)) return false;
-        tc_after();
-        if (L.hadamard) {  // O out of the rotated basis
-          float x[kD];
-          load_o(tm_o, x);
-          rotate_row(x);
+  for (int ph = 0; ph < 2; ++ph) {
+    const bool in_a = ph == 0;
+    int left = in_a ? tiles_a : n - tiles_a;
+    if (left == 0) continue;
+    if (have_o) {  // every product of phase A must be in O, and have read Q
+      if (!mbar_wait_warp(bar.o_done + 8 * w, 0, abort)) return false;
+      tc_after();
+      if (L.hadamard) {  // O out of the rotated basis
+        float x[kD];
+        load_o(tm_o, x);
+        rotate_row(x);
 #pragma unroll
-          for (int c = 0; c < kD; c += 32) tmem_st32(tm_o + c, reinterpret_cast<const uint32_t*>(x) + c);
-          tmem_wait_st();
-        }
+        for (int c = 0; c < kD; c += 32) tmem_st32(tm_o + c, reinterpret_cast<const uint32_t*>(x) + c);
+        tmem_wait_st();
       }
-      cs = load_query(p, it, r, row, qtile, in_a);
-      fence_async_smem();
-      tc_before();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(bar.q_ready + 8 * w);
     }
-    // what the tile needs is worked out before the wait for its scores
-    const int at = in_a ? (it.a0 + k) * kTile : it.tile_b(k) * kTile;  // its first position or entry
-    const bool masked = in_a ? at + kTile > it.q || at <= last_lo_a : at + kTile - 1 > first_hi || at <= last_lo_b;
-    if (!mbar_wait_warp(bar.s_full + 8 * w, j & 1, abort)) return false;
-    tc_after();
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      uint32_t s[64];
-      tmem_ld32(tm_s + 64 * h, s);
-      tmem_ld32(tm_s + 64 * h + 32, s + 32);
-      tmem_wait_ld(s);
-      tmem_wait_ld(s + 32);
-      if (masked) {
-#pragma unroll
-        for (int e = 0; e < 64; e += 32) {
-          const int c = at + 64 * h + e;
-          if (in_a)
-            mask_chunk(s + e, shuffle_bits(bit_range(lo_a + 1 - c, it.q - c), per));
-          else
-            mask_chunk(s + e, bit_range(lo_b + 1 - c, hi_b + 1 - c) | bit_range(0 - c, min(it.first_e, hi_b + 1) - c));
-        }
-      }
-      if (in_a || !bf16) softmax_half<false>(s, h, cs, st, tm_s, tm_o, j > 0);
-      else softmax_half<true>(s, h, cs, st, tm_s, tm_o, j > 0);
-    }
-    tmem_wait_st();
+    const float cs = load_query(p, it, r, row, qtile, in_a);
+    fence_async_smem();
     tc_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar.p_ready + 8 * w);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar.q_ready + 8 * w);
+    // the tile's first position (phase A) or entry, and the next one's. A row
+    // sees positions or entries in (lo, hi), and entries below `sinks`; all of
+    // the item's rows see all of a tile that lies in (most_lo, least_hi).
+    int k = k_first + (in_a ? 0 : tiles_a * step);
+    int at = in_a ? (it.a0 + k) * kTile : it.tile_b(k) * kTile;
+    const int lo = in_a ? lo_a : lo_b, hi = in_a ? it.q : hi_b + 1;
+    const int most_lo = in_a ? last_lo_a : last_lo_b, least_hi = in_a ? it.q : first_hi + 1;
+    const int sinks = in_a ? 0 : min(it.first_e, hi_b + 1);
+    const bool half_type = in_a || !bf16;
+#pragma unroll 1
+    for (; left > 0; --left) {
+      const bool masked = at + kTile > least_hi || at <= most_lo;
+      if (!mbar_wait_warp(s_full, parity, abort)) return false;
+      tc_after();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t s[64];
+        tmem_ld32(tm_s + 64 * h, s);
+        tmem_ld32(tm_s + 64 * h + 32, s + 32);
+        tmem_wait_ld(s);
+        tmem_wait_ld(s + 32);
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 64; e += 32) {
+            const int c = at + 64 * h + e;
+            const uint32_t bits = bit_range(lo + 1 - c, hi - c) | bit_range(0 - c, sinks - c);
+            mask_chunk(s + e, in_a ? shuffle_bits(bits, per) : bits);
+          }
+        }
+        if (half_type) softmax_half<false>(s, h, cs, st, tm_s, tm_o, have_o);
+        else softmax_half<true>(s, h, cs, st, tm_s, tm_o, have_o);
+      }
+      tmem_wait_st();
+      tc_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(p_ready);
+      have_o = true;
+      parity ^= 1u;
+      k += step;
+      at = in_a ? at + step * kTile : it.tile_b(k) * kTile;
+    }
   }
   // ---- the row's output or part
   const bool there = r < it.rows;
   float x[kD];
   if (n > 0) {
-    const bool last_a = it.slot_tile(w, n - 1) < it.nA, first_a = it.slot_tile(w, 0) < it.nA;
-    if (!mbar_wait_warp(bar.o_done + 8 * w, first_a && !last_a ? 1 : 0, abort)) return false;
+    const bool last_a = tiles_a == n;
+    if (!mbar_wait_warp(bar.o_done + 8 * w, tiles_a > 0 && !last_a ? 1 : 0, abort)) return false;
     tc_after();
     load_o(tm_o, x);
     if (L.hadamard && last_a) rotate_row(x);
@@ -1013,7 +1021,7 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
   }
   if (!there) return true;
   if (it.parts > 1) {
-    const int64_t rec = p.part0[it.i] + ((int64_t)it.h * it.rows + r) * it.parts + it.part + (it.both ? 0 : w);
+    const int64_t rec = p.e[it.i].part0 + ((int64_t)it.h * it.rows + r) * it.parts + it.part + (it.both ? 0 : w);
     float4* o = reinterpret_cast<float4*>(p.ws_o + rec * kD);
 #pragma unroll
     for (int c = 0; c < kD / 4; ++c) o[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
@@ -1021,7 +1029,7 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
     return true;
   }
   const float f = 1.f / st.l;  // every row sees its own token
-  const int64_t at = ((int64_t)(p.in_off[it.i] + r / it.ngr) * p.num_q_heads + it.h * it.ngr + r % it.ngr) * kD;
+  const int64_t at = ((int64_t)(p.e[it.i].off + r / it.ngr) * p.num_q_heads + it.h * it.ngr + r % it.ngr) * kD;
   if (p.out_dtype == KVQ_F32) {
     float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at);
 #pragma unroll
@@ -1245,16 +1253,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(const
   const int lane = threadIdx.x & 31;
   const int64_t g = (int64_t)blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
   if (g >= p.merge_rows) return;
-  int lo = 0, hi = p.nseq - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.merge0[mid] <= g) lo = mid;
-    else hi = mid - 1;
-  }
-  const int i = lo, ngr = p.num_q_heads / p.L.num_kv_heads, rows = p.t_new[i] * ngr;
-  const int parts = chunk_parts(p.splits[i]);
-  const int64_t x = g - p.merge0[i];  // h * rows + r
-  const int64_t rec = p.part0[i] + x * parts;
+  const int i = p.entry_of_merge((int)g), ngr = p.num_q_heads / p.L.num_kv_heads, rows = p.e[i].t * ngr;
+  const int parts = chunk_parts(p.e[i].splits);
+  const int64_t x = g - p.e[i].merge0;  // h * rows + r
+  const int64_t rec = p.e[i].part0 + x * parts;
   float M = -INFINITY;
   for (int e = lane; e < parts; e += 32) M = fmaxf(M, p.ws_ml[rec + e].x);
 #pragma unroll
@@ -1274,7 +1276,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(const
   }
   const float f = 1.f / l;
   const int h = (int)(x / rows), r = (int)(x % rows);
-  const int64_t at = ((int64_t)(p.in_off[i] + r / ngr) * p.num_q_heads + h * ngr + r % ngr) * kD + 4 * lane;
+  const int64_t at = ((int64_t)(p.e[i].off + r / ngr) * p.num_q_heads + h * ngr + r % ngr) * kD + 4 * lane;
   if (p.out_dtype == KVQ_F32) {
     *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at) =
         make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
