@@ -32,6 +32,7 @@ struct kvq_cache {
   int64_t err_off;                // int32 device error word
   int64_t uslots_off;             // int32 [max_batch][num_kv_heads] slots per unit (decode -> combine)
   int32_t slots;                  // partial slots per (sequence, query head)
+  int64_t partials;               // rows of the split-partial workspace
   int32_t sm_count;
   uint64_t launches = 0;          // kernels enqueued by calls on this cache (kvq_cache_kernel_launches)
   // host mirror [num_layers][max_batch]: quantized keys, key ring tokens,
@@ -151,7 +152,9 @@ struct Plan {
   std::vector<int64_t> blocks_off, ring_k_off, ring_v_off, sink_k_off, sink_v_off, record_bytes, pt_off;
   int64_t max_blocks, lens_off, err_off, uslots_off, ws_o_off, ws_ml_off, total;
   int32_t slots, max_pages;
+  int64_t partials;  // rows of the split-partial workspace
 };
+constexpr int64_t kMinPartials = 30720;
 
 Plan make_plan(const kvq_config* c) {
   using kvq::round_up;
@@ -196,11 +199,13 @@ Plan make_plan(const kvq_config* c) {
       std::min<int64_t>(p.max_blocks, KVQ_MAX_SPLITS) + 1,
       kvq::kMmaConsumers *
           (std::min<int64_t>(p.max_blocks + (c->residual + kvq::kResChunk - 1) / kvq::kResChunk + 1, 64) + 2));
-  const int64_t partials = (int64_t)c->max_batch * c->num_q_heads * p.slots;
+  // (and, for chunk attention, for a few ranges of some hundred query tokens of
+  // a small cache: 300 tokens of 32 heads in 3 ranges are 28,800 rows)
+  p.partials = std::max<int64_t>((int64_t)c->max_batch * c->num_q_heads * p.slots, kMinPartials);
   p.ws_o_off = off;
-  off = round_up(off + partials * D * 4, 256);
+  off = round_up(off + p.partials * D * 4, 256);
   p.ws_ml_off = off;
-  off = round_up(off + partials * 8, 256);
+  off = round_up(off + p.partials * 8, 256);
   p.total = off;
   return p;
 }
@@ -470,7 +475,7 @@ kvq_status plan_chunk(const kvq_cache* c, kvq::ChunkParams& p) {
   constexpr double kRecordTiles = 7e-5;  // tiles' time to write and read one part of a row
   const kvq_config& cfg = c->cfg;
   const int ngr = cfg.num_q_heads / cfg.num_kv_heads, hkv = cfg.num_kv_heads;
-  const int64_t sms = std::max(1, c->sm_count), room = (int64_t)cfg.max_batch * cfg.num_q_heads * c->slots;
+  const int64_t sms = std::max(1, c->sm_count), room = c->partials;
   struct Entry {
     int64_t rows, units, tiles;  // tiles of an average unit
     int32_t seq, s, q, qv, n, t, off;
@@ -532,14 +537,12 @@ kvq_status plan_chunk(const kvq_cache* c, kvq::ChunkParams& p) {
   bool best_alt = false;
   double best_cost = 1e300;
   for (int alternate = 1; alternate >= 0; --alternate)
-    for (int64_t ranges = 1; ranges <= kMostRanges && (ranges == 1 || most / ranges >= kLeast); ++ranges) {
-      const int64_t target = std::max<int64_t>(kLeast, (most + ranges - 1) / ranges);
+    for (int64_t target = std::max(most, kLeast); target >= kLeast; target -= 1 + target / 16)
       if (cut(target, alternate != 0) && cost < best_cost) {
         best_cost = cost;
         best = target;
         best_alt = alternate != 0;
       }
-    }
   if (best == 0) return fail(KVQ_ERR_UNSUPPORTED, "too many query rows in one call");
   (void)cut(best, best_alt);
   return KVQ_OK;
@@ -975,6 +978,7 @@ kvq_status kvq_cache_create(const kvq_config* cfg, void* dev_arena, size_t arena
   c->err_off = plan.err_off;
   c->uslots_off = plan.uslots_off;
   c->slots = plan.slots;
+  c->partials = plan.partials;
   c->pt_off = plan.pt_off;
   c->max_pages = plan.max_pages;
   if (cfg->page_blocks > 0) {
