@@ -67,7 +67,7 @@ constexpr int kBarOff = kVOff + kVStages * kTileBytes;
 constexpr int kBarBytes = 8 * (2 * kKStages + 2 * kVStages + 4 * 2 + 2 * kRawStages + 1);
 constexpr int kRawOff = kBarOff + 256, kRawBytes = 34304;  // packed parts: at most 18,432 bytes each
 constexpr int kSmemBytes = kRawOff + kRawBytes + 1024;     // + alignment of the base to 1024
-static_assert(kBarBytes <= kRawOff - kBarOff && kSmemBytes + 128 <= 227 * 1024, "shared memory of one CTA");
+static_assert(kBarBytes <= 8 * 32 && kBarBytes <= kRawOff - kBarOff && kSmemBytes + 128 <= 227 * 1024, "shared memory of one CTA");
 constexpr int kTmemS = 0, kTmemO = 256;           // columns of slot 0; slot 1 is 128 further
 constexpr float kOffset = 6.f, kMost = 16384.f;
 constexpr long long kWaitCycles = 4000000000LL;
@@ -234,7 +234,8 @@ struct alignas(64) ChunkMaps {
 // ------------------------------------------------------------------ the item
 struct Item {
   int i, b, h;          // table entry, sequence, KV head
-  int ngr, rows, r0;    // query heads per KV head, rows of the unit, first row of the item
+  int ngr, lg, rows, r0;  // query heads per KV head (1, 2, 4 or 8) and its logarithm, rows of the unit, first row of the item
+  int off;              // the sequence's first row in k, v, q and out
   bool both;            // both slots walk every tile (else alternate tiles)
   int t0, t1;           // first and last new token of the item's rows
   int s, q, n;          // sinks, quantized positions, ring tokens
@@ -244,6 +245,10 @@ struct Item {
   int part, parts;      // first part of the item, parts of the unit's rows
   int first_e;          // phase B entries below this stay visible outside the window
 
+  // row of q and out of row r of the unit
+  __device__ __forceinline__ int64_t row_of(const ChunkParams& p, int r) const {
+    return (int64_t)(off + (r >> lg)) * p.num_q_heads + (h << lg) + (r & (ngr - 1));
+  }
   __device__ __forceinline__ int tile_b(int k) const {  // phase B tile of k >= nA
     const int j = k - nA;
     return b_sink ? (j == 0 ? 0 : b0 + j - 1) : b0 + j;
@@ -260,6 +265,8 @@ __device__ __forceinline__ Item find_item(const ChunkParams& p, int idx) {
   it.i = lo;
   it.b = p.e[lo].seq;
   it.ngr = p.num_q_heads / hkv;
+  it.lg = __ffs(it.ngr) - 1;
+  it.off = p.e[lo].off;
   it.rows = p.e[lo].t * it.ngr;
   it.both = p.e[lo].splits > 0;
   const int ns = abs(p.e[lo].splits), tiles = (it.rows + 2 * kRows - 1) / (2 * kRows);
@@ -268,8 +275,8 @@ __device__ __forceinline__ Item find_item(const ChunkParams& p, int idx) {
   x /= ns;
   it.h = x % hkv;
   it.r0 = (tiles - 1 - x / hkv) * 2 * kRows;  // the rows that see most first
-  it.t0 = it.r0 / it.ngr;
-  it.t1 = (min(it.r0 + 2 * kRows, it.rows) - 1) / it.ngr;
+  it.t0 = it.r0 >> it.lg;
+  it.t1 = (min(it.r0 + 2 * kRows, it.rows) - 1) >> it.lg;
   it.s = p.e[lo].s;
   it.q = p.e[lo].q;
   it.n = p.e[lo].n;
@@ -706,6 +713,7 @@ __device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t til
 }
 
 // ------------------------------------------------------------------- softmax
+constexpr float kRsqrtD = (float)(1.0 / 11.313708498984761);  // 1 / sqrt(128)
 // Radix-2 butterflies of one row held by one thread, then 1/sqrt(128): x . H.
 __device__ __forceinline__ void rotate_row(float (&x)[kD]) {
 #pragma unroll
@@ -717,72 +725,92 @@ __device__ __forceinline__ void rotate_row(float (&x)[kD]) {
         x[c] = a + b;
         x[c + w] = a - b;
       }
-  const float s = (float)(1.0 / 11.313708498984761);
 #pragma unroll
-  for (int c = 0; c < kD; ++c) x[c] *= s;
+  for (int c = 0; c < kD; ++c) x[c] *= kRsqrtD;
 }
 
-// Writes this thread's query row into its slot's A tile: phase A (fp16, times
-// a power of two, rotated for a Hadamard cache) or phase B (as it is), with
-// the sign of the softmax scale. Returns log2-units per score.
-__device__ __forceinline__ float load_query(const ChunkParams& p, const Item& it, int r, int row, uint32_t tile,
-                                            bool phase_a) {
-  const bool there = r < it.rows;
+// The warp's 32 query rows into its slot's A tile, two rows at a time (16 lanes
+// with 8 channels each, so that loads are whole rows): phase A (fp16, times a
+// power of two per row, rotated for a Hadamard cache) or phase B (as they are),
+// with the sign of the softmax scale. Returns log2-units per score of the row
+// of this lane.
+__device__ __forceinline__ float load_queries(const ChunkParams& p, const Item& it, int first, uint32_t tile,
+                                              int tile_row, bool phase_a) {
+  const int lane = threadIdx.x & 31, ch = lane & 15, up = lane >> 4;
   const bool bf16 = p.L.kv_dtype == KVQ_BF16;
-  const int64_t at = (int64_t)(p.e[it.i].off + r / it.ngr) * p.num_q_heads + it.h * it.ngr + r % it.ngr;
-  const uint4* src = reinterpret_cast<const uint4*>(p.q) + at * 16;
-  const uint32_t dst = tile + row * 128;
   const float scale = fabsf(p.scale_log2);
   const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-  if (!phase_a) {
+  float cs = fmaxf(scale, 1e-37f);  // never 0: a masked score is -inf times this
+  const uint32_t dst = tile + (ch >> 3) * kHalf;
+  auto chunk = [&](int i) {  // of row 2i + up
+    const int row = tile_row + 2 * i + up;
+    return dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+  };
+  uint4 v[16];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const uint4 v = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-      sts16(dst + (c >> 3) * kHalf + (((c & 7) ^ (row & 7)) << 4), v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
-    }
-    return fmaxf(scale, 1e-37f);  // never 0: a masked score is -inf times this
+  for (int i = 0; i < 16; ++i) {  // all loads before any use
+    const int r = first + 2 * i + up;
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < it.rows) v[i] = __ldg(reinterpret_cast<const uint4*>(p.q) + it.row_of(p, r) * 16 + ch);
   }
-  float x[kD];
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    const uint4 v = there ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
+  for (int i = 0; i < 16; ++i) sts16(chunk(i), v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
+  if (phase_a) {
+    // in place (a lane reads what it wrote); kept rolled: this runs once per
+    // item, from a cold instruction cache
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      const uint4 q = lds16(chunk(i));
+      uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      float x[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (bf16) {
-        x[8 * c + 2 * e] = __uint_as_float(w[e] << 16);
-        x[8 * c + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-      } else {
-        const float2 f = __half22float2(half2_of(w[e]));
-        x[8 * c + 2 * e] = f.x;
-        x[8 * c + 2 * e + 1] = f.y;
+      for (int e = 0; e < 4; ++e) {
+        float2 f;
+        if (bf16) f = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+        else f = __half22float2(half2_of(w[e]));
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
       }
+      if (p.L.hadamard) {
+        // butterflies of half-width 1, 2, 4 in the lane, 8 .. 64 across the 16 lanes
+#pragma unroll
+        for (int d = 1; d < 8; d *= 2)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if ((e & d) == 0) {
+              const float a = x[e], b = x[e + d];
+              x[e] = a + b;
+              x[e + d] = a - b;
+            }
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float y = __shfl_xor_sync(0xffffffffu, x[e], d);
+            x[e] = (ch & d) ? y - x[e] : x[e] + y;
+          }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= kRsqrtD;
+      }
+      float mx = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
+#pragma unroll
+      for (int d = 1; d < 16; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      // the row's largest value to [8, 16)
+      const int ex = mx > 0.f ? min(100, 3 - ((int)(__float_as_uint(mx) >> 23) - 127)) : 0;
+      const float f = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = pack2<false>(x[2 * e] * f, x[2 * e + 1] * f);
+      const float c = fmaxf(scale * __uint_as_float((uint32_t)(127 - ex) << 23), 1e-37f);
+      const float c0 = __shfl_sync(0xffffffffu, c, 0), c1 = __shfl_sync(0xffffffffu, c, 16);
+      if ((lane >> 1) == i) cs = (lane & 1) ? c1 : c0;
+      sts16(chunk(i), w[0], w[1], w[2], w[3]);
     }
   }
-  if (p.L.hadamard) rotate_row(x);
-  float mx = 0.f;
-#pragma unroll
-  for (int c = 0; c < kD; ++c) mx = fmaxf(mx, fabsf(x[c]));
-  // the row's largest value to [8, 16)
-  const int e = mx > 0.f ? min(100, 3 - ((int)(__float_as_uint(mx) >> 23) - 127)) : 0;
-  const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = pack2<false>(x[8 * c + 2 * j] * up, x[8 * c + 2 * j + 1] * up);
-    sts16(dst + (c >> 3) * kHalf + (((c & 7) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
-  }
-  return fmaxf(scale * __uint_as_float((uint32_t)(127 - e) << 23), 1e-37f);
+  return cs;
 }
 
-__device__ __forceinline__ void load_o(uint32_t tm_o, float (&x)[kD]) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(x);
-#pragma unroll
-  for (int c = 0; c < kD; c += 32) tmem_ld32(tm_o + c, r + c);
-#pragma unroll
-  for (int c = 0; c < kD; c += 32) tmem_wait_ld(r + c);
-}
 // Bits [a, b) of a word (bounds outside 0 .. 32 are cut off).
 __device__ __forceinline__ uint32_t bit_range(int a, int b) {
   const uint32_t below_b = b <= 0 ? 0u : b >= 32 ? 0xffffffffu : (1u << b) - 1u;
@@ -923,7 +951,7 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
   const LayerView& L = p.L;
   const int row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
   const int r = it.r0 + (it.both ? w * kRows : 0) + row;
-  const int t = min(r, it.rows - 1) / it.ngr;  // the row's new token
+  const int t = min(r, it.rows - 1) >> it.lg;  // the row's new token
   const bool bf16 = L.kv_dtype == KVQ_BF16;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
   const uint32_t tm_s = tmem + lanes + kTmemS + w * kTile, tm_o = tmem + lanes + kTmemO + w * kD;
@@ -947,19 +975,7 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
     const bool in_a = ph == 0;
     int left = in_a ? tiles_a : n - tiles_a;
     if (left == 0) continue;
-    if (have_o) {  // every product of phase A must be in O, and have read Q
-      if (!mbar_wait_warp(bar.o_done + 8 * w, 0, abort)) return false;
-      tc_after();
-      if (L.hadamard) {  // O out of the rotated basis
-        float x[kD];
-        load_o(tm_o, x);
-        rotate_row(x);
-#pragma unroll
-        for (int c = 0; c < kD; c += 32) tmem_st32(tm_o + c, reinterpret_cast<const uint32_t*>(x) + c);
-        tmem_wait_st();
-      }
-    }
-    const float cs = load_query(p, it, r, row, qtile, in_a);
+    const float cs = load_queries(p, it, r & ~31, qtile, row & ~31, in_a);
     fence_async_smem();
     tc_before();
     __syncwarp();
@@ -1005,47 +1021,69 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
       k += step;
       at = in_a ? at + step * kTile : it.tile_b(k) * kTile;
     }
-  }
-  // ---- the row's output or part
-  const bool there = r < it.rows;
-  float x[kD];
-  if (n > 0) {
-    const bool last_a = tiles_a == n;
-    if (!mbar_wait_warp(bar.o_done + 8 * w, tiles_a > 0 && !last_a ? 1 : 0, abort)) return false;
+    // every product of the phase in O (and done with the queries)
+    if (!mbar_wait_warp(bar.o_done + 8 * w, in_a || tiles_a == 0 ? 0 : 1, abort)) return false;
     tc_after();
-    load_o(tm_o, x);
-    if (L.hadamard && last_a) rotate_row(x);
-  } else {
+    if (in_a && L.hadamard) {  // O out of the rotated basis
+      float x[kD];
 #pragma unroll
-    for (int c = 0; c < kD; ++c) x[c] = 0.f;
+      for (int c = 0; c < kD; c += 32) tmem_ld32(tm_o + c, reinterpret_cast<uint32_t*>(x) + c);
+#pragma unroll
+      for (int c = 0; c < kD; c += 32) tmem_wait_ld(reinterpret_cast<uint32_t*>(x) + c);
+      rotate_row(x);
+#pragma unroll
+      for (int c = 0; c < kD; c += 32) tmem_st32(tm_o + c, reinterpret_cast<const uint32_t*>(x) + c);
+      tmem_wait_st();
+    }
   }
-  if (!there) return true;
-  if (it.parts > 1) {
-    const int64_t rec = p.e[it.i].part0 + ((int64_t)it.h * it.rows + r) * it.parts + it.part + (it.both ? 0 : w);
-    float4* o = reinterpret_cast<float4*>(p.ws_o + rec * kD);
+  // ---- the row's output or part: through the warp's share of the query tile
+  // (8 KB, free now), so that stores are whole rows; 16-bit rows at once, fp32
+  // ones in two halves of 64 channels
+  const int lane = threadIdx.x & 31, first = r & ~31;
+  const uint32_t mine = qtile + (row & ~31) * 256, to = mine + lane * 256;
+  const bool parts = it.parts > 1, wide = parts || p.out_dtype == KVQ_F32, ob = p.out_dtype == KVQ_BF16;
+  const int64_t rec0 = p.e[it.i].part0 + (int64_t)it.h * it.rows * it.parts + it.part + (it.both ? 0 : w);
+  if (parts && r < it.rows) p.ws_ml[rec0 + (int64_t)r * it.parts] = make_float2(st.m, st.l);
+  const float f = parts ? 1.f : 1.f / st.l;  // every row sees its own token
+  for (int half = 0; half < (wide ? 2 : 1); ++half) {
+    __syncwarp();
+#pragma unroll 1
+    for (int c = 0; c < (wide ? 4 : 8); ++c) {  // 16 channels: a 16-byte chunk e at e ^ (lane % 16)
+      uint32_t y[16];
+      if (n > 0) {
+        tmem_ld16(tm_o + 64 * half + 16 * c, y);
+        tmem_wait_ld16(y);
+      } else {
 #pragma unroll
-    for (int c = 0; c < kD / 4; ++c) o[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-    p.ws_ml[rec] = make_float2(st.m, st.l);
-    return true;
-  }
-  const float f = 1.f / st.l;  // every row sees its own token
-  const int64_t at = ((int64_t)(p.e[it.i].off + r / it.ngr) * p.num_q_heads + it.h * it.ngr + r % it.ngr) * kD;
-  if (p.out_dtype == KVQ_F32) {
-    float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at);
+        for (int e = 0; e < 16; ++e) y[e] = 0u;
+      }
 #pragma unroll
-    for (int c = 0; c < kD / 4; ++c)
-      o[c] = make_float4(x[4 * c] * f, x[4 * c + 1] * f, x[4 * c + 2] * f, x[4 * c + 3] * f);
-  } else {
-    uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at);
-    const bool ob = p.out_dtype == KVQ_BF16;
+      for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+      if (wide) {
 #pragma unroll
-    for (int c = 0; c < kD / 8; ++c) {
-      uint32_t y[4];
+        for (int e = 0; e < 4; ++e)
+          sts16(to + (((4 * c + e) ^ (lane & 15)) << 4), y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+      } else {
+        uint32_t z[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        y[e] = ob ? pack2<true>(x[8 * c + 2 * e] * f, x[8 * c + 2 * e + 1] * f)
-                  : pack2<false>(x[8 * c + 2 * e] * f, x[8 * c + 2 * e + 1] * f);
-      o[c] = make_uint4(y[0], y[1], y[2], y[3]);
+        for (int e = 0; e < 8; ++e) {
+          const float a = __uint_as_float(y[2 * e]), b = __uint_as_float(y[2 * e + 1]);
+          z[e] = ob ? pack2<true>(a, b) : pack2<false>(a, b);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          sts16(to + (((2 * c + e) ^ (lane & 15)) << 4), z[4 * e], z[4 * e + 1], z[4 * e + 2], z[4 * e + 3]);
+      }
+    }
+    __syncwarp();
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+      const int l = 2 * i + (lane >> 4), rr = first + l, c = lane & 15;
+      const uint4 v = lds16(mine + l * 256 + ((c ^ (l & 15)) << 4));
+      if (rr >= it.rows) continue;
+      if (parts) reinterpret_cast<uint4*>(p.ws_o + (rec0 + (int64_t)rr * it.parts) * kD + 64 * half)[c] = v;
+      else if (wide) reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.out) + it.row_of(p, rr) * kD + 64 * half)[c] = v;
+      else reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + it.row_of(p, rr) * kD)[c] = v;
     }
   }
   return true;
@@ -1174,27 +1212,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
     bar.drain = at;
   }
   const Item it = find_item(p, blockIdx.x);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kKStages; ++i) {
-      mbar_init(bar.k_full + 8 * i, kProducers / 32);
-      mbar_init(bar.k_empty + 8 * i, 1);
-    }
-    for (int i = 0; i < kVStages; ++i) {
-      mbar_init(bar.v_full + 8 * i, kProducers / 32);
-      mbar_init(bar.v_empty + 8 * i, 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar.s_full + 8 * i, 1);
-      mbar_init(bar.p_ready + 8 * i, 4);
-      mbar_init(bar.o_done + 8 * i, 1);
-      mbar_init(bar.q_ready + 8 * i, 4);
-    }
-    for (int i = 0; i < kRawStages; ++i) {
-      mbar_init(bar.raw_full + 8 * i, 1);
-      mbar_init(bar.raw_empty + 8 * i, 2 * kProducers / 32);
-    }
-    mbar_init(bar.drain, 1);
-    s_abort = 0;
+  if (warp == 17) {  // a barrier per lane
+    const int lane = threadIdx.x & 31;
+    const uint32_t at = smem + kBarOff + 8 * lane;
+    const bool produced = at >= bar.k_full && at < bar.k_full + 8 * kKStages || at >= bar.v_full && at < bar.v_full + 8 * kVStages;
+    const bool slot = at >= bar.p_ready && at < bar.p_ready + 16 || at >= bar.q_ready && at < bar.q_ready + 16;
+    const bool raw_empty = at >= bar.raw_empty && at < bar.raw_empty + 8 * kRawStages;
+    if (8 * lane < kBarBytes) mbar_init(at, produced ? kProducers / 32 : slot ? 4 : raw_empty ? 2 * kProducers / 32 : 1);
+    if (lane == 0) s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 16) {
