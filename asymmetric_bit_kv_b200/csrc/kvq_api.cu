@@ -480,8 +480,7 @@ kvq_status plan_chunk(const kvq_cache* c, kvq::ChunkParams& p) {
     int64_t rows, units, tiles;  // tiles of an average unit
     int32_t seq, s, q, qv, n, t, off;
   };
-  thread_local std::vector<Entry> es;
-  es.resize(p.nseq);
+  thread_local Entry es[KVQ_MAX_BATCH];
   int64_t most = 0;
   for (int x = 0; x < p.nseq; ++x) {
     Entry& e = es[x];
@@ -496,7 +495,7 @@ kvq_status plan_chunk(const kvq_cache* c, kvq::ChunkParams& p) {
     most = std::max(most, e.tiles);
   }
   // the longest units first, so that the last wave ends with short ones
-  std::stable_sort(es.begin(), es.end(), [](const Entry& a, const Entry& b) { return a.tiles > b.tiles; });
+  std::stable_sort(es, es + p.nseq, [](const Entry& a, const Entry& b) { return a.tiles > b.tiles; });
   for (int x = 0; x < p.nseq; ++x) {
     const Entry& e = es[x];
     p.e[x].seq = e.seq, p.e[x].s = e.s, p.e[x].q = e.q, p.e[x].qv = e.qv, p.e[x].n = e.n, p.e[x].t = e.t;
@@ -1197,7 +1196,7 @@ kvq_status kvq_chunk_attention(kvq_cache* c, int32_t layer, const void* k, const
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.out_dtype = out_dtype;
   p.num_q_heads = cfg.num_q_heads;
-  p.window = window;
+  p.window = window < (1 << 30) ? window : 0;  // no sequence reaches token 2^30
   p.sink_tokens = cfg.sink_tokens;
   p.tokens = (int32_t)total;
   p.nseq = 0;

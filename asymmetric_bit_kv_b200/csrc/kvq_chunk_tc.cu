@@ -23,9 +23,10 @@
 // tiles, 10, 11, 14, 15 value tiles (each kind on two of the four schedulers),
 // 16 issues the MMAs, 17 copies packed parts (18, 19 idle: registers move between
 // whole warpgroups, setmaxnreg 144 + 144 + 72 + 72 + 48 = 5 x 96). The hot
-// loops are kept short (32 columns, one row of codes at a time): four roles
-// share an SM's instruction caches, and unrolled whole tiles spent most of
-// their time waiting for instructions.
+// loops are kept short (half a row of scores, one row of codes at a time) and
+// what runs once per item is kept rolled: four roles share an SM's instruction
+// caches, and unrolled whole tiles spent most of their time waiting for
+// instructions.
 //
 // Operands. Phase A: codes become fp16 in three instructions per pair (mask
 // into the mantissa of 1024, subtract, one fma q*d + m: the only rounding).
@@ -34,9 +35,10 @@
 // tiles with 128-byte swizzle. A word's codes come out in extraction order
 // (i, i + n/2), which permutes the tokens of a key tile: value rows are stored
 // in the same order (their channels are put back by one permute per pair).
-// Queries are scaled by a power of two per row (exact but for
-// subnormals), so that any bf16 query fits fp16. Phase B: keys, values,
-// queries and probabilities in the kv dtype, keys K-major.
+// Queries are scaled by a power of two per row (exact but for subnormals), so
+// that any bf16 query fits fp16. Phase B: keys, values, queries and
+// probabilities in the kv dtype, keys K-major.
+//
 // Softmax: probabilities are 2^(z - m + 6) with m a whole number that is raised
 // only when the sum of 64 of a row's probabilities reaches 2^14: one pass over
 // the scores without their maximum; rescaling O and what the tile has written
@@ -67,9 +69,10 @@ constexpr int kBarOff = kVOff + kVStages * kTileBytes;
 constexpr int kBarBytes = 8 * (2 * kKStages + 2 * kVStages + 4 * 2 + 2 * kRawStages + 1);
 constexpr int kRawOff = kBarOff + 256, kRawBytes = 34304;  // packed parts: at most 18,432 bytes each
 constexpr int kSmemBytes = kRawOff + kRawBytes + 1024;     // + alignment of the base to 1024
-static_assert(kBarBytes <= 8 * 32 && kBarBytes <= kRawOff - kBarOff && kSmemBytes + 128 <= 227 * 1024, "shared memory of one CTA");
+static_assert(kBarBytes <= 8 * 32 && kBarBytes <= kRawOff - kBarOff, "a barrier per lane of a warp");
+static_assert(kSmemBytes + 128 <= 227 * 1024, "shared memory of one CTA");
 constexpr int kTmemS = 0, kTmemO = 256;           // columns of slot 0; slot 1 is 128 further
-constexpr float kOffset = 6.f, kMost = 16384.f;
+constexpr float kOffset = 6.f, kMost = 16384.f;  // of the probabilities: see above
 constexpr long long kWaitCycles = 4000000000LL;
 
 // ------------------------------------------------------------- PTX helpers
@@ -79,6 +82,9 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {  // and arrive
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -234,7 +240,8 @@ struct alignas(64) ChunkMaps {
 // ------------------------------------------------------------------ the item
 struct Item {
   int i, b, h;          // table entry, sequence, KV head
-  int ngr, lg, rows, r0;  // query heads per KV head (1, 2, 4 or 8) and its logarithm, rows of the unit, first row of the item
+  int ngr, lg;          // query heads per KV head (1, 2, 4 or 8) and the logarithm
+  int rows, r0;         // rows of the unit, first row of the item
   int off;              // the sequence's first row in k, v, q and out
   bool both;            // both slots walk every tile (else alternate tiles)
   int t0, t1;           // first and last new token of the item's rows
@@ -422,13 +429,14 @@ __device__ bool copy_parts(const ChunkParams& p, const Item& it, uint32_t smem, 
     const uint32_t rb = (uint32_t)L.record_bytes;
     if (G == 32) {
       const bool two = pos + 32 < it.q;
-      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "r"(two ? 2 * rb : rb) : "memory");
+      mbar_expect_tx(full, two ? 2 * rb : rb);
       bulk_g2s(dst, rec, rb, full);
       if (two) bulk_g2s(dst + rb, record_ptr(L, it.b, it.h, pos / G + 1), rb, full);
     } else {
-      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "r"(raw.tile + L.tile_bytes) : "memory");
+      mbar_expect_tx(full, raw.tile + L.tile_bytes);
       if (raw.tile) bulk_g2s(dst, rec + L.rec_ksz_off, kD * 4, full);
-      bulk_g2s(dst + raw.tile, rec + L.tile0_off + (G == 128 ? ((pos >> 6) & 1) * L.tile_bytes : 0), L.tile_bytes, full);
+      const int64_t tile = G == 128 ? ((pos >> 6) & 1) * L.tile_bytes : 0;
+      bulk_g2s(dst + raw.tile, rec + L.tile0_off + tile, L.tile_bytes, full);
     }
   }
   return true;
@@ -436,7 +444,10 @@ __device__ bool copy_parts(const ChunkParams& p, const Item& it, uint32_t smem, 
 
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t lds4(uint32_t addr) {
@@ -660,7 +671,7 @@ __device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t til
   const int ch = kt & 15;
   const uint4* sink_p = reinterpret_cast<const uint4*>(sink) + unit * KVQ_MAX_SINKS * 16 + ch;
   const uint4* ring_p = reinterpret_cast<const uint4*>(ring) + unit * L.residual * 16 + ch;
-  const uint4* new_p = reinterpret_cast<const uint4*>(fresh) + ((int64_t)p.e[it.i].off * L.num_kv_heads + it.h) * 16 + ch;
+  const uint4* new_p = reinterpret_cast<const uint4*>(fresh) + ((int64_t)it.off * L.num_kv_heads + it.h) * 16 + ch;
   const int64_t stride = (int64_t)L.num_kv_heads * 16;
   const int held = it.s + it.n, last = held + it.t1;
   const int slot0 = it.q % L.residual;  // ring slot of the first ring token
@@ -674,13 +685,12 @@ __device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t til
     if (e0 >= held && e0 - held + kTile <= p.e[it.i].t) {
       if ((kt & 31) == 0) {
         if (kt == 0) {
-          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(kTileBytes) : "memory");
+          mbar_expect_tx(bar, kTileBytes);
 #pragma unroll
           for (int half = 0; half < 2; ++half)
             asm volatile(
-                "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                    dst + half * kHalf),
-                "l"(map), "r"(it.h * kD + 64 * half), "r"(p.e[it.i].off + e0 - held), "r"(bar)
+                "cp.async.bulk.tensor.2d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                ::"r"(dst + half * kHalf), "l"(map), "r"(it.h * kD + 64 * half), "r"(it.off + e0 - held), "r"(bar)
                 : "memory");
         } else {
           mbar_arrive(bar);
@@ -877,8 +887,8 @@ __device__ __forceinline__ void probabilities(const uint32_t* s, float cs, float
   }
 }
 // Half a tile (64 columns, scores in s). The probabilities go by the m so far.
-// Their sum tells whether that was good enough: below 2^kMost none of them
-// passes fp16's range. Else (always on a row's first tile, hardly ever later) m
+// Their sum tells whether that was good enough: below kMost none of them passes
+// fp16's range. Else (always on a row's first tile, hardly ever later) m
 // is raised to the maximum, what was written is rescaled and the half is
 // computed again. Packed pairs go over the columns 32h .. of the scores already
 // read.
@@ -1082,8 +1092,9 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
       const uint4 v = lds16(mine + l * 256 + ((c ^ (l & 15)) << 4));
       if (rr >= it.rows) continue;
       if (parts) reinterpret_cast<uint4*>(p.ws_o + (rec0 + (int64_t)rr * it.parts) * kD + 64 * half)[c] = v;
-      else if (wide) reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.out) + it.row_of(p, rr) * kD + 64 * half)[c] = v;
-      else reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + it.row_of(p, rr) * kD)[c] = v;
+      else if (wide)
+        reinterpret_cast<uint4*>(static_cast<float*>(p.out) + it.row_of(p, rr) * kD + 64 * half)[c] = v;
+      else reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + it.row_of(p, rr) * kD)[c] = v;
     }
   }
   return true;
@@ -1189,7 +1200,8 @@ __device__ bool issue_products(const ChunkParams& p, const Item& it, uint32_t sm
   return true;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ ChunkMaps maps) {
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ ChunkMaps maps) {
   extern __shared__ uint8_t raw[];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -1215,10 +1227,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_tc_kernel(const __grid_cons
   if (warp == 17) {  // a barrier per lane
     const int lane = threadIdx.x & 31;
     const uint32_t at = smem + kBarOff + 8 * lane;
-    const bool produced = at >= bar.k_full && at < bar.k_full + 8 * kKStages || at >= bar.v_full && at < bar.v_full + 8 * kVStages;
-    const bool slot = at >= bar.p_ready && at < bar.p_ready + 16 || at >= bar.q_ready && at < bar.q_ready + 16;
-    const bool raw_empty = at >= bar.raw_empty && at < bar.raw_empty + 8 * kRawStages;
-    if (8 * lane < kBarBytes) mbar_init(at, produced ? kProducers / 32 : slot ? 4 : raw_empty ? 2 * kProducers / 32 : 1);
+    auto in = [&](uint32_t first, int n) { return at >= first && at < first + 8 * n; };
+    // arrivals: of the key or value warps, of a slot's warps, of one thread or a commit
+    const bool produced = in(bar.k_full, kKStages) || in(bar.v_full, kVStages);
+    const bool slot = in(bar.p_ready, 2) || in(bar.q_ready, 2), raw_empty = in(bar.raw_empty, kRawStages);
+    if (8 * lane < kBarBytes) mbar_init(at, produced ? kProducers / 32 : slot ? 4 : raw_empty ? kProducers / 16 : 1);
     if (lane == 0) s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1364,7 +1377,8 @@ cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream) {
   chunk_tc_kernel<<<p.items, kThreads, kSmemBytes, stream>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.merge_rows == 0) return e;
-  chunk_combine_kernel<<<(unsigned)((p.merge_rows + kCombineWarps - 1) / kCombineWarps), 32 * kCombineWarps, 0, stream>>>(p);
+  const unsigned merges = (unsigned)((p.merge_rows + kCombineWarps - 1) / kCombineWarps);
+  chunk_combine_kernel<<<merges, 32 * kCombineWarps, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -404,8 +404,8 @@ KVQ_API kvq_status kvq_dequant(kvq_cache* cache, int32_t layer, int32_t seq, int
                        float* k_out, float* v_out, void* stream);
 
 /* Device-side failures recorded since the last call, then cleared: bit 0 =
- * a decode kernel gave up a bounded wait on its copy pipeline (its partial
- * results are invalid); bit 1 = a decode CTA found an empty work range in
+ * a decode or chunk kernel gave up a bounded wait on its pipeline (its results
+ * are invalid); bit 1 = a decode CTA found an empty work range in
  * its plan (results invalid; not expected). Synchronous: waits for the
  * device to finish its work. No counterpart on the pages: a diagnostic of
  * this library.                                                           */
@@ -416,7 +416,8 @@ KVQ_API kvq_status kvq_device_errors(kvq_cache* cache, int32_t* flags);
  * ring write, plus the quantize kernel when a ring flushes, plus a page-table
  * update when pages are taken; decode: the decode kernel and the combine
  * kernel; a fused step's flush kernel on a step whose rings are full;
- * dequant). For accounting, e.g. a benchmark that reads it
+ * chunk attention: its kernel, plus the merge when some rows have several
+ * parts; fork: one per 32 layers and 64 destinations; dequant). For accounting, e.g. a benchmark that reads it
  * around a timed region. No counterpart on the pages.
  * - cache, count: non-null (else KVQ_ERR_INVALID_ARG). Host only.          */
 KVQ_API kvq_status kvq_cache_kernel_launches(const kvq_cache* cache, uint64_t* count);

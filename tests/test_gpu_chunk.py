@@ -82,7 +82,7 @@ def test_chunks_of_a_growing_cache(fmt):
     cache.close()
 
 
-@pytest.mark.parametrize("window", [1, 2, 31, 64, 100, 127, 128, 129, 500, 1 << 29])
+@pytest.mark.parametrize("window", [1, 2, 31, 64, 100, 127, 128, 129, 500, 1 << 29, 2 ** 31 - 1])
 @pytest.mark.parametrize("fmt", ["k2v4_g64", "k4v4_g32_gv128", "bq2", "k2v2_g32_mha", "split_windows", "rot_channel_k4v4"])
 def test_sliding_window(fmt, window):
     cache = make(fmt, 3)
