@@ -472,6 +472,8 @@ kvq_status check_window(const kvq_cache* c, int32_t window) {
 // uncut 3.46 waves run as 4; 2 ranges each run as 7 half waves, 10% sooner.)
 kvq_status plan_chunk(const kvq_cache* c, kvq::ChunkParams& p) {
   constexpr int64_t kItemTiles = 4, kLeast = 4, kMostRanges = 64;
+  // (shared pages: half of a row's slots are the decode kernel's)
+  const int64_t most_ranges = p.slots > 0 ? std::max(1, std::min<int32_t>(kMostRanges, p.slots / 4)) : kMostRanges;
   constexpr double kRecordTiles = 7e-5;  // tiles' time to write and read one part of a row
   const kvq_config& cfg = c->cfg;
   const int ngr = cfg.num_q_heads / cfg.num_kv_heads, hkv = cfg.num_kv_heads;
@@ -489,7 +491,8 @@ kvq_status plan_chunk(const kvq_cache* c, kvq::ChunkParams& p) {
     const int64_t unit_rows = 2 * kvq::kChunkSlotRows;
     e.units = hkv * ((e.rows + unit_rows - 1) / unit_rows);
     const int64_t seen = p.window > 0 ? (int64_t)p.window + unit_rows / ngr : INT64_MAX;
-    const int64_t exact = std::min<int64_t>(seen, e.s + e.n + (e.rows > unit_rows ? (e.t + 1) / 2 : e.t));
+    const int64_t exact =
+        p.slots > 0 ? 0 : std::min<int64_t>(seen, e.s + e.n + (e.rows > unit_rows ? (e.t + 1) / 2 : e.t));
     const int64_t quant = std::min<int64_t>(e.q, std::max<int64_t>(0, seen - e.n));
     e.tiles = (quant + kvq::kChunkTile - 1) / kvq::kChunkTile + (exact + kvq::kChunkTile - 1) / kvq::kChunkTile;
     most = std::max(most, e.tiles);
@@ -508,7 +511,7 @@ kvq_status plan_chunk(const kvq_cache* c, kvq::ChunkParams& p) {
     int64_t items = 0, records = 0, merged = 0, work = 0, longest = 0;
     for (int x = 0; x < p.nseq; ++x) {
       const Entry& e = es[x];
-      const int64_t ns = std::min<int64_t>(kMostRanges, (e.tiles + target - 1) / target);
+      const int64_t ns = std::min<int64_t>(most_ranges, (e.tiles + target - 1) / target);
       const bool alt = alternate && e.rows <= kvq::kChunkSlotRows && e.tiles > 1;
       p.e[x].splits = (int32_t)(alt ? -ns : ns);
       const int parts = kvq::chunk_parts(p.e[x].splits);
@@ -520,7 +523,7 @@ kvq_status plan_chunk(const kvq_cache* c, kvq::ChunkParams& p) {
       items += e.units * ns;
       work += e.units * ns * each;
       longest = std::max(longest, each);
-      if (parts > 1) {
+      if (parts > 1 || p.slots > 0) {
         merged += e.rows * hkv;
         records += e.rows * hkv * parts;
       }
@@ -545,6 +548,85 @@ kvq_status plan_chunk(const kvq_cache* c, kvq::ChunkParams& p) {
   if (best == 0) return fail(KVQ_ERR_UNSUPPORTED, "too many query rows in one call");
   (void)cut(best, best_alt);
   return KVQ_OK;
+}
+
+// Decode of sequences that share pages (a fork's copies, until they differ):
+// runs of neighbouring sequences of the batch whose first pages are the same
+// ones. The run's shared positions are processed once for all of its query
+// rows by the chunk-attention kernel, which leaves its parts beside the decode
+// kernel's partials; the decode kernel then starts behind them, as behind a
+// window. Fills p (launch table), slots and lo (first position left to the
+// decode kernel, per sequence), and returns true if that is worth its launch.
+//
+// Both sides as measured, in ns: the decode kernel takes 3 per 128-token tile,
+// KV head and sequence; the chunk kernel 25 us and 2350 per tile and head that
+// an SM processes, 8 us more to rotate and 0.22 per part of a row that is
+// written and merged. Decode of n copies of a prompt of 16 blocks to a page, 32
+// query and 8 KV heads, K2 V4, each on its own / together, in us: 16 x 8200
+// 48 / 61, 32 x 8200 77 / 69, 32 x 32800 226 / 87; 32 KV heads, K2 V2 in groups
+// of 32: 8 x 4000 52 / 61, 16 x 4000 91 / 69, 32 x 8200 294 / 108, 4 x 32800
+// 151 / 157, 32 x 32800 1060 / 198.
+bool plan_shared(const kvq_cache* c, int layer, int batch, int32_t slot_cap, kvq::ChunkParams& p,
+                 kvq::SharedSlots& slots, int32_t* lo) {
+  constexpr double kDecodeTile = 3, kLaunch = 25000, kTile = 2350, kRotate = 8000, kRecord = 0.22;
+  constexpr int kLeastRun = 3;  // two sequences: no faster together
+  const kvq_config& cfg = c->cfg;
+  const int page = cfg.page_blocks * cfg.group_k;  // positions
+  const size_t base = (size_t)layer * cfg.max_batch;
+  auto row_of = [&](int b) { return &c->pt_host[(base + b) * c->max_pages]; };
+  double alone = 0, together = kLaunch + (cfg.hadamard ? kRotate : 0);
+  p.nseq = 0;
+  for (int b = 0; b < batch;) {
+    // the run from b with the most (sequences - 1) x pages
+    int pages = c->pages_held[base + b], end = b + 1, run = 1, held = 0;
+    int64_t gain = 0;
+    for (; end < batch && pages > 0; ++end) {
+      const int32_t *x = row_of(b), *y = row_of(end);
+      const int most = std::min(pages, c->pages_held[base + end]);
+      int same = 0;
+      while (same < most && x[same] == y[same]) ++same;
+      pages = same;
+      if ((int64_t)(end - b) * pages > gain) {
+        gain = (int64_t)(end - b) * pages;
+        run = end - b + 1;
+        held = pages;
+      }
+    }
+    for (int i = b; i < b + run; ++i) lo[i] = run >= kLeastRun ? held * page : 0;
+    if (run >= kLeastRun) {
+      kvq::ChunkEntry& e = p.e[p.nseq++];
+      e.seq = e.off = b;
+      e.s = e.n = 0;
+      e.q = e.qv = held * page;
+      e.t = run;
+      const double tiles = (double)e.q / kvq::kChunkTile * cfg.num_kv_heads;
+      const int rows = run * (cfg.num_q_heads / cfg.num_kv_heads), unit_rows = 2 * kvq::kChunkSlotRows;
+      alone += kDecodeTile * tiles * run;
+      together += kTile * tiles * ((rows + unit_rows - 1) / unit_rows) / std::max(1, c->sm_count);
+    }
+    b += run;
+  }
+  if (alone <= together) return false;
+  p.window = 0;
+  p.num_q_heads = cfg.num_q_heads;
+  p.slots = slot_cap;
+  if (plan_chunk(c, p) != KVQ_OK) {
+    g_last_error.clear();
+    return false;
+  }
+  for (int x = 0; x < p.nseq; ++x)
+    together += kRecord * p.e[x].t * cfg.num_q_heads * kvq::chunk_parts(p.e[x].splits);
+  if (alone <= together) return false;
+  p.merge_rows = 0;
+  slots.first = 0;
+  std::memset(slots.parts, 0, batch);
+  for (int x = 0; x < p.nseq; ++x) slots.first = std::max(slots.first, kvq::chunk_parts(p.e[x].splits));
+  for (int x = 0; x < p.nseq; ++x) {
+    const int parts = kvq::chunk_parts(p.e[x].splits);
+    p.e[x].part0 = slots.first - parts;
+    std::memset(slots.parts + p.e[x].off, parts, p.e[x].t);
+  }
+  return true;
 }
 
 // kvq_fork_sequence after its argument checks.
@@ -758,16 +840,22 @@ kvq_status enqueue_decode(kvq_cache* c, int32_t layer, const void* new_k, const 
     // concatenated and cut into one contiguous range of equal cost per CTA,
     // one CTA per resident slot (fewer if there is little work).
     const kvq::MmaPlan mp = kvq::make_mma_plan(L, Hv);
-    const int per_sm = kvq::mma_ctas_per_sm(L, mp, Hv, window > 0);
     thread_local WindowTables wt;
+    thread_local kvq::ChunkParams cp;
+    thread_local kvq::SharedSlots shared_slots;
+    const bool shared = cfg.page_blocks > 0 && !qg && !scratch && window == 0 && batch >= 3 &&
+                        kvq::chunk_tc_supported(L) && slot_cap >= 4 * kMmaConsumers &&
+                        plan_shared(c, layer, batch, slot_cap, cp, shared_slots, wt.lo);
+    const bool windowed = window > 0 || shared;
+    const int per_sm = kvq::mma_ctas_per_sm(L, mp, Hv, windowed);
     for (int b = 0; b < batch; ++b) {
       const size_t i = (size_t)layer * cfg.max_batch + b;
       p.nblk[b] = c->q_len[i] / L.tile_tokens;  // tile items of the quantized blocks
       p.nres[b] = c->n_len[i];
       int32_t nres = p.nres[b];
-      if (window > 0) {
+      if (windowed) {
         // the tiles and ring chunks below the window's first position are no items
-        const int32_t lo = std::max(0, c->q_len[i] + c->n_len[i] - window);
+        const int32_t lo = shared ? wt.lo[b] : std::max(0, c->q_len[i] + c->n_len[i] - window);
         wt.lo[b] = lo;
         wt.tile0[b] = std::min(lo, c->q_len[i]) / L.tile_tokens;
         wt.chunk0[b] = std::max(0, lo - c->q_len[i]) / kvq::kResChunk;
@@ -779,10 +867,29 @@ kvq_status enqueue_decode(kvq_cache* c, int32_t layer, const void* new_k, const 
     p.persistent = 1;
     p.slots = slot_cap;
     p.after_flush = after_flush ? 1 : 0;
+    e = cudaSuccess;
+    if (shared) {
+      // the parts of the shared pages, in a row's first slots
+      cp.L = L;
+      cp.k = cp.v = cp.q = q;  // (no new tokens)
+      cp.out = nullptr;
+      cp.ws_o = p.ws_o;
+      cp.ws_ml = p.ws_ml;
+      cp.err = p.err;
+      cp.scale_log2 = p.scale_log2;
+      cp.out_dtype = KVQ_F32;
+      cp.sink_tokens = 0;
+      cp.tokens = batch;
+      e = kvq::launch_chunk_tc(cp, st);
+      p.ws_o += (int64_t)shared_slots.first * kHeadDim;
+      p.ws_ml += shared_slots.first;
+      slot_cap -= shared_slots.first;
+    }
     plan_cta_starts(p, batch, cfg.num_kv_heads, (int64_t)std::max(1, c->sm_count) * per_sm, slot_cap);
-    e = kvq::launch_decode_mma(p, mp, window > 0 ? &wt : nullptr, st);
-    if (e == cudaSuccess) e = kvq::launch_combine(p, st);
-    if (e == cudaSuccess) c->launches += 2;  // the decode kernel and the combine
+    if (e == cudaSuccess) e = kvq::launch_decode_mma(p, mp, windowed ? &wt : nullptr, st);
+    if (e == cudaSuccess) e = kvq::launch_combine(p, st, shared ? &shared_slots : nullptr);
+    // the decode kernel and the combine, and the kernel of the shared pages
+    if (e == cudaSuccess) c->launches += shared ? 3 : 2;
   } else {
     // Split plan (host mirror): blocks per split chosen to minimise (waves
     // of CTAs) x (blocks per CTA + a fixed per-CTA overhead), with at most
@@ -1198,6 +1305,7 @@ kvq_status kvq_chunk_attention(kvq_cache* c, int32_t layer, const void* k, const
   p.num_q_heads = cfg.num_q_heads;
   p.window = window < (1 << 30) ? window : 0;  // no sequence reaches token 2^30
   p.sink_tokens = cfg.sink_tokens;
+  p.slots = 0;
   p.tokens = (int32_t)total;
   p.nseq = 0;
   int32_t off = 0;

@@ -49,6 +49,12 @@ struct ChunkParams {
   int32_t nseq;         // entries
   int32_t items;        // work items of all entries
   int32_t merge_rows;
+  // Shared pages (decode of forked sequences; 0: chunk attention). An entry is
+  // then a run of sequences off .. off + t - 1 with one query token each, whose
+  // first q positions lie in pages that all of them hold: its rows see those
+  // positions and nothing else, and part j of a row of q goes to record
+  // row * slots + part0 + j, beside the decode kernel's partials of the row.
+  int32_t slots;
   ChunkEntry e[KVQ_MAX_BATCH];
 
   // The entry that work item (merge row) x belongs to.

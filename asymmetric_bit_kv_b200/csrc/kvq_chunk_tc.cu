@@ -295,7 +295,7 @@ __device__ __forceinline__ Item find_item(const ChunkParams& p, int idx) {
   const int low_b = p.window > 0 ? max(0, it.s + after) : 0;
   it.b0 = low_b / kTile;
   it.b_sink = it.first_e > 0 && it.b0 > 0 ? 1 : 0;
-  it.nB = (it.s + it.n + it.t1 + kTile) / kTile - it.b0 + it.b_sink;
+  it.nB = p.slots > 0 ? 0 : (it.s + it.n + it.t1 + kTile) / kTile - it.b0 + it.b_sink;
   const int64_t total = it.nA + it.nB;
   it.k0 = (int)(total * sp / ns);
   it.k1 = (int)(total * (sp + 1) / ns);
@@ -1051,9 +1051,14 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
   // ones in two halves of 64 channels
   const int lane = threadIdx.x & 31, first = r & ~31;
   const uint32_t mine = qtile + (row & ~31) * 256, to = mine + lane * 256;
-  const bool parts = it.parts > 1, wide = parts || p.out_dtype == KVQ_F32, ob = p.out_dtype == KVQ_BF16;
-  const int64_t rec0 = p.e[it.i].part0 + (int64_t)it.h * it.rows * it.parts + it.part + (it.both ? 0 : w);
-  if (parts && r < it.rows) p.ws_ml[rec0 + (int64_t)r * it.parts] = make_float2(st.m, st.l);
+  const bool parts = it.parts > 1 || p.slots > 0;
+  const bool wide = parts || p.out_dtype == KVQ_F32, ob = p.out_dtype == KVQ_BF16;
+  const int64_t rec0 = p.e[it.i].part0 + it.part + (it.both ? 0 : w);
+  auto record = [&](int rr) {
+    return rec0 + (p.slots > 0 ? it.row_of(p, rr) * p.slots : ((int64_t)it.h * it.rows + rr) * it.parts);
+  };
+  // (sum and output are 2^kOffset times those of the maximum m)
+  if (parts && r < it.rows) p.ws_ml[record(r)] = make_float2(st.m - kOffset, st.l);
   const float f = parts ? 1.f : 1.f / st.l;  // every row sees its own token
   for (int half = 0; half < (wide ? 2 : 1); ++half) {
     __syncwarp();
@@ -1091,7 +1096,7 @@ __device__ bool softmax_slot(const ChunkParams& p, const Item& it, int w, uint32
       const int l = 2 * i + (lane >> 4), rr = first + l, c = lane & 15;
       const uint4 v = lds16(mine + l * 256 + ((c ^ (l & 15)) << 4));
       if (rr >= it.rows) continue;
-      if (parts) reinterpret_cast<uint4*>(p.ws_o + (rec0 + (int64_t)rr * it.parts) * kD + 64 * half)[c] = v;
+      if (parts) reinterpret_cast<uint4*>(p.ws_o + record(rr) * kD + 64 * half)[c] = v;
       else if (wide)
         reinterpret_cast<uint4*>(static_cast<float*>(p.out) + it.row_of(p, rr) * kD + 64 * half)[c] = v;
       else reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + it.row_of(p, rr) * kD)[c] = v;
@@ -1223,6 +1228,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bar.raw_empty = at, at += 8 * kRawStages;
     bar.drain = at;
   }
+  // the merge of the parts may be scheduled (it waits for this grid before it
+  // reads): 2 us of 123 for 300 new tokens
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Item it = find_item(p, blockIdx.x);
   if (warp == 17) {  // a barrier per lane
     const int lane = threadIdx.x & 31;
@@ -1288,6 +1296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Merges the parts of a row (parts > 1): a warp per row, four channels a lane.
 constexpr int kCombineWarps = 8;
 __global__ void __launch_bounds__(32 * kCombineWarps) chunk_combine_kernel(const __grid_constant__ ChunkParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t g = (int64_t)blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
   if (g >= p.merge_rows) return;
@@ -1378,8 +1387,16 @@ cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess || p.merge_rows == 0) return e;
   const unsigned merges = (unsigned)((p.merge_rows + kCombineWarps - 1) / kCombineWarps);
-  chunk_combine_kernel<<<merges, 32 * kCombineWarps, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(merges);
+  cfg.blockDim = dim3(32 * kCombineWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_combine_kernel, p);
 }
 
 }  // namespace kvq

@@ -335,8 +335,15 @@ __device__ __forceinline__ void merge_into(MergeState& a, const MergeState& b) {
   a.M = M;
 }
 
-template <int WPH>
-__global__ void __launch_bounds__(32 * (WPH > 4 ? WPH : 4)) combine_kernel(CombineParams p) {
+// First slot of sequence b's partials: 0, or where the parts of its shared
+// pages begin.
+__device__ __forceinline__ int first_slot(const SharedSlots& x, int b) { return x.first - x.parts[b]; }
+__device__ __forceinline__ int first_slot(const NoShared&, int) { return 0; }
+__device__ __forceinline__ int own_slot(const SharedSlots& x) { return x.first; }
+__device__ __forceinline__ int own_slot(const NoShared&) { return 0; }
+
+template <int WPH, typename Shared>
+__global__ void __launch_bounds__(32 * (WPH > 4 ? WPH : 4)) combine_kernel(CombineParams p, Shared shared) {
   constexpr int kWarps = WPH > 4 ? WPH : 4, kHeads = kWarps / WPH;
   __shared__ MergeState s_st[kWarps][32];
   // wait for the decode grid this launch depends on (no-op without one)
@@ -359,7 +366,9 @@ __global__ void __launch_bounds__(32 * (WPH > 4 ? WPH : 4)) combine_kernel(Combi
       S = (nblk + p.blocks_per_split - 1) / p.blocks_per_split + 1;
     }
   }
-  const int64_t base = ((int64_t)b * p.num_q_heads + hq) * p.slots;
+  const int from = first_slot(shared, b);
+  if (active) S += own_slot(shared) - from;
+  const int64_t base = ((int64_t)b * p.num_q_heads + hq) * p.slots + from;
   const float2* ml_p = p.ws_ml + base;
   const float4* o_p = reinterpret_cast<const float4*>(p.ws_o + base * D) + lane;  // slot s at o_p[s * D / 4]
   MergeState st{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
@@ -509,11 +518,11 @@ cudaError_t launch_decode(const DecodeParams& p, int max_splits, cudaStream_t st
   return launch_combine(p, stream);
 }
 
-cudaError_t launch_combine(const DecodeParams& p, cudaStream_t stream) {
+cudaError_t launch_combine(const DecodeParams& p, cudaStream_t stream, const SharedSlots* shared) {
   if (p.batch <= 0) return cudaSuccess;
   // Warps per (sequence, query head): enough that each merges at most 16
   // slots (one round of loads), from the most slots a unit can use.
-  const int most = p.persistent ? p.max_unit_slots : p.slots;
+  const int most = (p.persistent ? p.max_unit_slots : p.slots) + (shared ? shared->first : 0);
   int wph = 1;
   while (wph < 32 && wph * 16 < most) wph *= 2;
   const int warps = wph > 4 ? wph : 4, heads = warps / wph;
@@ -530,17 +539,22 @@ cudaError_t launch_combine(const DecodeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = p.persistent ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const CombineParams cp{p.ws_o,         p.ws_ml,          p.out,           p.unit_slots,
+  const int64_t first = shared ? shared->first : 0;  // (the decode kernel's slots come after the shared parts)
+  const CombineParams cp{p.ws_o - first * kHeadDim, p.ws_ml - first,         p.out,           p.unit_slots,
                          p.L.lens,       p.out_dtype,      p.num_q_heads,   p.L.num_kv_heads,
                          p.slots,        p.L.group_k,      p.blocks_per_split, p.persistent, p.L.hadamard,
                          p.q_heads,      p.q_rows,         p.window};
   switch (wph) {
-    case 1: return cudaLaunchKernelEx(&cfg, combine_kernel<1>, cp);
-    case 2: return cudaLaunchKernelEx(&cfg, combine_kernel<2>, cp);
-    case 4: return cudaLaunchKernelEx(&cfg, combine_kernel<4>, cp);
-    case 8: return cudaLaunchKernelEx(&cfg, combine_kernel<8>, cp);
-    case 16: return cudaLaunchKernelEx(&cfg, combine_kernel<16>, cp);
-    default: return cudaLaunchKernelEx(&cfg, combine_kernel<32>, cp);
+#define KVQ_COMBINE(W)                                                                    \
+  return shared ? cudaLaunchKernelEx(&cfg, combine_kernel<W, SharedSlots>, cp, *shared) \
+                : cudaLaunchKernelEx(&cfg, combine_kernel<W, NoShared>, cp, NoShared{})
+    case 1: KVQ_COMBINE(1);
+    case 2: KVQ_COMBINE(2);
+    case 4: KVQ_COMBINE(4);
+    case 8: KVQ_COMBINE(8);
+    case 16: KVQ_COMBINE(16);
+    default: KVQ_COMBINE(32);
+#undef KVQ_COMBINE
   }
 }
 

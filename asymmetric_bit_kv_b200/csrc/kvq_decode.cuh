@@ -169,8 +169,19 @@ struct CombineParams {
   int32_t window;           // split mode: the first split starts at the window's first block
 };
 
-// The log-sum-exp combine of the partial slots (after the decode kernel).
-cudaError_t launch_combine(const DecodeParams& p, cudaStream_t stream);
+// Pages shared by neighbouring sequences (persistent mode): the decode kernel's
+// slots of a row begin at `first`, and the parts[b] slots before them hold the
+// parts of the sequence's shared pages (0: none).
+struct SharedSlots {
+  int32_t first;
+  uint8_t parts[KVQ_MAX_BATCH];
+};
+struct NoShared {};
+
+// The log-sum-exp combine of the partial slots (after the decode kernel);
+// shared: where the parts of shared pages are, or null. p.ws_o and p.ws_ml
+// point at the decode kernel's first slot.
+cudaError_t launch_combine(const DecodeParams& p, cudaStream_t stream, const SharedSlots* shared = nullptr);
 
 // Device memory for the split partials other than the arena's workspace.
 struct StaticScratch {

@@ -390,6 +390,10 @@ KVQ_API kvq_status kvq_decode_step_window(kvq_cache* cache, int32_t layer, const
  *   the partly filled last page, the rings, the sinks and the lengths are
  *   copied. Fails with KVQ_ERR_CAPACITY, changing nothing, if some layer's
  *   pool cannot give every destination its page.
+ *   kvq_decode_attention and kvq_decode_step read pages that three or more
+ *   neighbouring sequences of the batch share once for all of them, where
+ *   that is faster (long prompts or many copies); the result is the same up
+ *   to the order of fp32 sums and the roundings kvq_chunk_attention states.
  * No counterpart on the pages: the cache side of parallel sampling.         */
 KVQ_API kvq_status kvq_fork_sequence(kvq_cache* cache, int32_t src, const int32_t* dsts, int32_t num_dsts,
                                      void* stream);
@@ -415,10 +419,11 @@ KVQ_API kvq_status kvq_device_errors(kvq_cache* cache, int32_t* flags);
  * when each call enqueues them: one per launch, whatever the kernel (append:
  * ring write, plus the quantize kernel when a ring flushes, plus a page-table
  * update when pages are taken; decode: the decode kernel and the combine
- * kernel; a fused step's flush kernel on a step whose rings are full;
- * chunk attention: its kernel, plus the merge when some rows have several
- * parts; fork: one per 32 layers and 64 destinations; dequant). For accounting, e.g. a benchmark that reads it
- * around a timed region. No counterpart on the pages.
+ * kernel, plus one when neighbouring sequences share enough pages; a fused
+ * step's flush kernel on a step whose rings are full; chunk attention: its
+ * kernel, plus the merge when some rows have several parts; fork: one per 32
+ * layers and 64 destinations; dequant). For accounting, e.g. a benchmark that
+ * reads it around a timed region. No counterpart on the pages.
  * - cache, count: non-null (else KVQ_ERR_INVALID_ARG). Host only.          */
 KVQ_API kvq_status kvq_cache_kernel_launches(const kvq_cache* cache, uint64_t* count);
 
