@@ -14,7 +14,8 @@
 // keys and values are dequantized once into shared memory as fp32 (rotated
 // back for a Hadamard cache), then each warp scores its rows with one lane
 // per token and accumulates the values with four channels per lane. Everything
-// is fp32. Bound by shared-memory loads and FMAs, as a plain fp32 kernel is.
+// is fp32. Bound by shared-memory loads and FMAs, as a plain fp32 kernel is:
+// 4096 new tokens over 32768 (32 query and 8 KV heads) take 1.55 s, 1.5 TFLOP/s.
 #include "kvq_chunk.cuh"
 
 namespace kvq {
