@@ -46,13 +46,16 @@
 // keep 14 + 6 binary orders below m before they turn subnormal.
 //
 // Measured (one B200; 32 query and 8 KV heads, K2 V4): 4096 new tokens over
-// 32768 in 2555 us, 915 TFLOP/s, 0.56 of the measured rate of large
-// products; a slot's chain (scores, exp2, probabilities, product) bounds it, with
-// the tensor and exp2 pipes at 47% each. 16 x 5 tokens over 8192: 114-120 us,
-// bound by expanding codes (2.1 us a tile). 2 x 300 tokens over 8190, rotated
-// per-token keys: 123 us, of which an item's start and end take a third.
+// 32768 in 2555 us, 915 TFLOP/s, 0.56 of the measured rate of large products; a
+// slot's chain (scores, exp2, probabilities, product) bounds it, with the
+// tensor and exp2 pipes at 47% each. 16 x 5 tokens over 8192: 114-120 us, 1.5 us
+// a tile by the same chain (103 with no codes expanded, 112 with half the
+// softmax) and 31 us of launch, start, end and merge. 2 x 300 tokens over 8190,
+// rotated per-token keys: 123 us, of which an item's start and end take a third.
 // Slower: tiles of 64 tokens (2774 us for the first of these), sixteen softmax
-// warps (2705), an issuing warp per slot (2720).
+// warps (2705), an issuing warp per slot (2720), the softmax skipped by warps
+// without rows (2893). Where the hot loops fall in the instruction caches moves
+// these figures by 5%.
 //
 // Every wait is bounded (~2 s): a thread that gives up sets the device error
 // word and an abort flag that ends the others' waits.
