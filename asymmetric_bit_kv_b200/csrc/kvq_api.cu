@@ -154,7 +154,7 @@ struct Plan {
   int32_t slots, max_pages;
   int64_t partials;  // rows of the split-partial workspace
 };
-constexpr int64_t kMinPartials = 30720;
+constexpr int64_t kMinPartials = 32768;
 
 Plan make_plan(const kvq_config* c) {
   using kvq::round_up;

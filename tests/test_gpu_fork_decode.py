@@ -27,12 +27,15 @@ def make(fmt, batch, cap):
                                hadamard=rot, page_blocks=P, pool_pages=6 * (-(-cap // (G * P)) + 1) + 8 * batch))
 
 
-def check(cache, q, out, what):
-    cfg = cache.cfg
+def check_one(cache, b, q, out, what="", scale=SCALE):
+    k, v = cached_tokens(cache, 0, b)
+    ref = attend(q[b:b + 1], k, v, k.shape[0] - 1, scale, 0, cache.cfg.sink_tokens)
+    assert_within(out[b:b + 1], ref, scale, cache.cfg, f"{what} sequence {b} of {k.shape[0]} tokens")
+
+
+def check(cache, q, out, what, scale=SCALE):
     for b in range(q.shape[0]):
-        k, v = cached_tokens(cache, 0, b)
-        ref = attend(q[b:b + 1], k, v, k.shape[0] - 1, SCALE, 0, cfg.sink_tokens)
-        assert_within(out[b:b + 1], ref, SCALE, cfg, f"{what} sequence {b} of {k.shape[0]} tokens")
+        check_one(cache, b, q, out, what, scale)
     assert cache.device_errors() == 0
 
 
@@ -107,6 +110,46 @@ def test_short_prompts_stay_on_the_decode_kernel():
     cache.fork_sequence(0, range(1, 8))
     q = tokens(8, cfg, gen)[2]
     assert launches(cache, lambda: cache.decode_attention(0, q, softmax_scale=SCALE))[0] == 2
+    cache.close()
+
+
+@pytest.mark.parametrize("fmt", ["k2v4_g64", "bq2"])
+@pytest.mark.parametrize("scale", [0.0, -0.05, 0.3])
+def test_softmax_scales(fmt, scale):
+    cache = make(fmt, 24, 13000)
+    cfg = cache.cfg
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    k, v, _ = tokens(12345, cfg, gen)
+    cache.append(0, k, v, [12345])
+    cache.fork_sequence(0, range(1, 24))
+    k, v, q = tokens(24 * 30, cfg, gen)
+    cache.append(0, k, v, [30] * 24)
+    n, out = launches(cache, lambda: cache.decode_attention(0, q[:24], out_dtype=cfg.kv_dtype, softmax_scale=scale))
+    assert n == 3
+    check(cache, q[:24], out, f"{fmt} scale {scale}", scale)
+    cache.close()
+
+
+def test_copies_of_copies():
+    """Copies made again over themselves and of one another: the pages' counts follow."""
+    cache = make("k2v4_g64", 20, 13000)
+    cfg = cache.cfg
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    k, v, _ = tokens(12345, cfg, gen)
+    cache.append(0, k, v, [12345])
+    for _ in range(3):
+        cache.fork_sequence(0, range(1, 20))
+        cache.fork_sequence(7, [0, 19])
+        cache.fork_sequence(19, [6, 8])
+        k, v, q = tokens(730, cfg, gen)
+        cache.append(0, k, v, [70 if b % 2 else 3 for b in range(20)])
+        out = cache.decode_attention(0, q[:20], out_dtype=cfg.kv_dtype, softmax_scale=SCALE)
+        check(cache, q[:20], out, "copies of copies")
+    for b in range(19):
+        cache.release_sequence(b)
+    out = cache.decode_attention(0, q[:20], out_dtype=cfg.kv_dtype, softmax_scale=SCALE)
+    assert not out[:19].any()
+    check_one(cache, 19, q, out)
     cache.close()
 
 
