@@ -159,6 +159,13 @@ def _need_shape(t: torch.Tensor, shape: tuple, name):
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
 
 
+def _window(window: int) -> int:
+    """window, refused where ctypes would cut it to 32 bits without a word."""
+    if not -2 ** 31 <= window < 2 ** 31:
+        raise ValueError(f"window {window} does not fit 32 bits")
+    return window
+
+
 @dataclass
 class CacheConfig:
     num_layers: int
@@ -334,7 +341,8 @@ class KVCache:
             softmax_scale = cfg.head_dim ** -0.5
         with self._on_device(k, v, q, out):
             _check(self.lib.kvq_chunk_attention(self.handle, layer, k.data_ptr(), v.data_ptr(), q.data_ptr(), out.data_ptr(),
-                                                _DTYPE_CODE[out.dtype], float(softmax_scale), arr, len(arr), window,
+                                                _DTYPE_CODE[out.dtype], float(softmax_scale), arr, len(arr),
+                                                _window(window),
                                                 _stream_ptr(stream)),
                    "kvq_chunk_attention")
         return out
@@ -350,8 +358,8 @@ class KVCache:
             softmax_scale = self.cfg.head_dim ** -0.5
         with self._on_device(q, out):
             _check(self.lib.kvq_decode_attention_window(self.handle, layer, q.data_ptr(), out.data_ptr(),
-                                                        _DTYPE_CODE[out.dtype], float(softmax_scale), q.shape[0], window,
-                                                        _stream_ptr(stream)),
+                                                        _DTYPE_CODE[out.dtype], float(softmax_scale), q.shape[0],
+                                                        _window(window), _stream_ptr(stream)),
                    "kvq_decode_attention_window")
         return out
 
@@ -370,7 +378,7 @@ class KVCache:
         with self._on_device(k, v, q, out):
             _check(self.lib.kvq_decode_step_window(self.handle, layer, k.data_ptr(), v.data_ptr(), q.data_ptr(),
                                                    out.data_ptr(), _DTYPE_CODE[out.dtype], float(softmax_scale), q.shape[0],
-                                                   window, _stream_ptr(stream)),
+                                                   _window(window), _stream_ptr(stream)),
                    "kvq_decode_step_window")
         return out
 

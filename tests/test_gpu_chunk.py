@@ -214,6 +214,20 @@ def test_captured_call_replays():
         cache.close()
 
 
+@pytest.mark.parametrize("fmt", ["k2v4_g64", "k2v2_g32_mha", "k2v2_g128"])
+@pytest.mark.parametrize("held", [0, 200])
+def test_a_long_first_chunk_of_few_heads(fmt, held):
+    """Cut into ranges by an average tile count that the first rows, which see little, do not reach: some of their
+    ranges are empty."""
+    cache = make(fmt, 1)
+    gen = torch.Generator(device="cuda").manual_seed(43)
+    k, v, _ = tokens(held, cache.cfg, gen)
+    cache.append(0, k, v, [held])
+    k, v, q = tokens(3500, cache.cfg, gen)
+    check(cache, k, v, q, [3500])
+    cache.close()
+
+
 def test_repeats_and_leaves_the_cache_alone():
     cache = make("k4v2_g64_paged", 2)
     gen = torch.Generator(device="cuda").manual_seed(41)

@@ -141,3 +141,19 @@ def test_refusals():
         cache.decode_attention_window(3, q, 5)
     assert cache.lengths(0, 0) == (0, 0)  # a refused step appends nothing
     cache.close()
+
+
+def test_windows_wider_than_32_bits_are_refused():
+    """(not cut to their low 32 bits)"""
+    cache = make("k2v4_g64", 2)
+    k, v, q = tokens(2, cache.cfg, torch.Generator(device="cuda").manual_seed(1))
+    cache.append(0, k, v, [1, 1])
+    for w in (2 ** 32 + 5, 2 ** 31, -2 ** 32 + 7):
+        with pytest.raises(ValueError, match="32 bits"):
+            cache.decode_attention_window(0, q, w)
+        with pytest.raises(ValueError, match="32 bits"):
+            cache.decode_step_window(0, k, v, q, w)
+        with pytest.raises(ValueError, match="32 bits"):
+            cache.chunk_attention(0, k, v, q, [1, 1], window=w)
+    assert cache.lengths(0, 0) == (0, 1)
+    cache.close()
