@@ -1266,25 +1266,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s_tmem;
   const LayerView& L = p.L;
   const int kt = ((warp >> 2) & 1) * 64 + (threadIdx.x & 63);  // of 128 key or value threads
-  if (warp < 8) {
+  // (all warps of a warpgroup must execute the same setmaxnreg: it comes before
+  // the key and value warps of a group part)
+  const int group = warp >> 2;
+  if (group < 2) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
-    (void)softmax_slot(p, it, warp >> 2, smem, tmem, bar, abort);
-  } else if (warp < 16 && !(warp & 2)) {
+    (void)softmax_slot(p, it, group, smem, tmem, bar, abort);
+  } else if (group < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    const bool ok = L.k_bits == 2   ? produce_keys<2>(p, it, smem, bar, kt, abort)
-                    : L.k_bits == 4 ? produce_keys<4>(p, it, smem, bar, kt, abort)
-                                    : produce_keys<8>(p, it, smem, bar, kt, abort);
-    if (ok)
-      (void)produce_exact<kKStages>(p, it, smem + kKOff, bar.k_full, bar.k_empty, L.sink_k, L.ring_k, p.k, &maps.k, kt,
-                                    abort);
-  } else if (warp < 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    const bool ok = L.v_bits == 2   ? produce_values<2>(p, it, smem, bar, kt, abort)
-                    : L.v_bits == 4 ? produce_values<4>(p, it, smem, bar, kt, abort)
-                                    : produce_values<8>(p, it, smem, bar, kt, abort);
-    if (ok)
-      (void)produce_exact<kVStages>(p, it, smem + kVOff, bar.v_full, bar.v_empty, L.sink_v, L.ring_v, p.v, &maps.v, kt,
-                                    abort);
+    if (!(warp & 2)) {
+      const bool ok = L.k_bits == 2   ? produce_keys<2>(p, it, smem, bar, kt, abort)
+                      : L.k_bits == 4 ? produce_keys<4>(p, it, smem, bar, kt, abort)
+                                      : produce_keys<8>(p, it, smem, bar, kt, abort);
+      if (ok)
+        (void)produce_exact<kKStages>(p, it, smem + kKOff, bar.k_full, bar.k_empty, L.sink_k, L.ring_k, p.k, &maps.k,
+                                      kt, abort);
+    } else {
+      const bool ok = L.v_bits == 2   ? produce_values<2>(p, it, smem, bar, kt, abort)
+                      : L.v_bits == 4 ? produce_values<4>(p, it, smem, bar, kt, abort)
+                                      : produce_values<8>(p, it, smem, bar, kt, abort);
+      if (ok)
+        (void)produce_exact<kVStages>(p, it, smem + kVOff, bar.v_full, bar.v_empty, L.sink_v, L.ring_v, p.v, &maps.v,
+                                      kt, abort);
+    }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == 16 && !issue_products(p, it, smem, tmem, bar, abort)) {

@@ -1,0 +1,34 @@
+"""What the tensor-core chunk kernel's source must keep to, checked without a GPU: rules of the instruction set whose
+violation may hang a GPU, so that no test runs into one."""
+
+import os
+import re
+
+from asymmetric_bit_kv_b200.build import CSRC
+
+SOURCE = open(os.path.join(CSRC, "kvq_chunk_tc.cu")).read()
+
+
+def _kernel():
+    at = SOURCE.index("chunk_tc_kernel(const __grid_constant__")
+    return SOURCE[at:SOURCE.index("\n}\n", at)]
+
+
+def test_a_warpgroup_executes_one_setmaxnreg():
+    """All threads of a warpgroup must execute the same setmaxnreg: each stands first in a branch on the warpgroup, and
+    the warpgroups' registers add up to what the block is launched with."""
+    kernel = _kernel()
+    assert "const int group = warp >> 2;" in kernel
+    found = re.findall(r"(?:if \((.*)\)|else) \{\n\s*asm volatile\(\"setmaxnreg\.(inc|dec)\.sync\.aligned\.u32 (\d+);", kernel)
+    assert len(found) == kernel.count("setmaxnreg.")
+    threads = int(re.search(r"kThreads = (\d+);", SOURCE)[1])
+    regs = []
+    for g in range(threads // 128):
+        for cond, _, n in found:
+            assert re.fullmatch(r"group < \d+|", cond), cond
+            if not cond or g < int(cond.split()[-1]):
+                regs.append(int(n))
+                break
+    assert len(regs) == threads // 128
+    launched = 65536 // threads // 8 * 8
+    assert sum(regs) <= launched * len(regs), (regs, launched)
