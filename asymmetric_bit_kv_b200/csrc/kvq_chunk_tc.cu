@@ -451,6 +451,9 @@ __device__ bool copy_parts(const ChunkParams& p, const Item& it, uint32_t smem, 
       bulk_g2s(dst + raw.tile, rec + L.tile0_off + tile, L.tile_bytes, full);
     }
   }
+  // (as in produce_exact: after an abort nobody else may wait for the last ones)
+  for (int v = max(0, 2 * tiles - raw.stages); v < 2 * tiles; ++v)
+    mbar_drain(bar.raw_full + 8 * (v % raw.stages), (v / raw.stages) & 1);
   return true;
 }
 
@@ -731,6 +734,11 @@ __device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t til
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
   }
+  // the last copies, in case of an abort: the block must not end under them
+  // (else they have been waited for by the time that the others end)
+  if (kt == 0)
+    for (int c = max(max(it.k0, it.nA), it.k1 - STAGES) - it.k0; c < it.k1 - it.k0; ++c)
+      mbar_drain(full + 8 * (c % STAGES), (c / STAGES) & 1);
   return true;
 }
 
@@ -1291,8 +1299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp == 16 && !issue_products(p, it, smem, tmem, bar, abort)) {
-      // let the products in flight finish before the tensor memory goes
+    if (warp == 16) {
+      (void)issue_products(p, it, smem, tmem, bar, abort);
+      // let the products in flight finish before the tensor memory goes,
+      // whoever gave up and when
       if (elect_one()) tc_commit(bar.drain);
       __syncwarp();
       mbar_drain(bar.drain, 0);

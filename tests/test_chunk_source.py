@@ -32,3 +32,25 @@ def test_a_warpgroup_executes_one_setmaxnreg():
     assert len(regs) == threads // 128
     launched = 65536 // threads // 8 * 8
     assert sum(regs) <= launched * len(regs), (regs, launched)
+
+
+def _function(name):
+    at = SOURCE.index(name + "(const ChunkParams& p")
+    return SOURCE[at:SOURCE.index("\n}\n", at)]
+
+
+def test_copies_in_flight_are_waited_for_however_an_item_ends():
+    """A warp that gives up a wait ends the others' waits, so that nobody may be left to wait for the last copies into
+    shared memory and the last products: whoever issued them does, after its last one, before the block ends."""
+    for name in ("copy_parts", "produce_exact"):
+        body = _function(name)
+        for exit_ in re.finditer("return (true|false);", body):
+            # between the last copy issued (or the failed wait) and the return
+            before = body[:exit_.start()]
+            at = max(before.rfind("bulk_g2s("), before.rfind("cp.async"), before.rfind("mbar_wait"))
+            assert "mbar_drain(" in before[at:], (name, exit_[0])
+    kernel = _kernel()
+    products = kernel[kernel.index("issue_products("):]
+    products = products[:products.index("copy_parts(")]
+    assert not re.search(r"!issue_products|if \([^)]*\) tc_commit\(bar\.drain\)", products.replace("if (elect_one())", ""))
+    assert products.index("tc_commit(bar.drain)") < products.index("mbar_drain(bar.drain, 0)")
