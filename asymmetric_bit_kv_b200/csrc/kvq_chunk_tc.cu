@@ -341,11 +341,42 @@ __host__ __device__ inline int place_of(int j, int per) {
 }
 __host__ __device__ inline int code_at(int c, int per) { return per == 4 ? c : ((c & 1) ? per / 2 : 0) + (c >> 1); }
 
+// The largest code of a group whose scale was rounded up may stand for more
+// than the largest fp16 number, 65504: it is taken as that. NaN stays.
+__device__ __forceinline__ __half2 limit2(__half2 y) { return __hmin2_nan(y, half2_of(0x7bff7bffu)); }
+// Whether some of a row's codes may: its groups' scales and zero points, each
+// twice in a word. Hardly ever, so that the row is then mended, by a function
+// that stays out of the hot loops: 16 x 5 tokens over 8192 take 119 us (without
+// any of this 120; with the function in line 132, the limit at every pair 138).
+template <int B>
+__device__ __forceinline__ bool past_fp16(const uint32_t (&s)[2], const uint32_t (&z)[2]) {
+  const __half2 top = __float2half2_rn((float)((1 << B) - 1));
+  return bits2(__hmax2(__hfma2(top, half2_of(s[0]), half2_of(z[0])), __hfma2(top, half2_of(s[1]), half2_of(z[1])))) ==
+         0x7c007c00u;
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __noinline__ void limit_row(uint32_t row) {
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {
+    const uint4 v = lds16(row + (c << 4));
+    sts16(row + (c << 4), bits2(limit2(half2_of(v.x))), bits2(limit2(half2_of(v.y))), bits2(limit2(half2_of(v.z))),
+          bits2(limit2(half2_of(v.w))));
+  }
+}
+
 // Expands 64 codes (2 * B words) into a 128-byte row of fp16 at `row`, chunk
 // c at c ^ x. sz(word, pair, s2, z2) gives the (scale, scale) and (zero, zero)
 // halves of the two codes of a pair.
-// NATURAL: the codes' own order instead, one more permute per pair.
-template <int B, bool NATURAL, class SZ>
+// NATURAL: the codes' own order instead, one more permute per pair. LIMIT: see
+// limit2; else the caller looks at the row's scales (past_fp16).
+template <int B, bool NATURAL, bool LIMIT, class SZ>
 __device__ __forceinline__ void expand_row(const uint32_t (&w)[2 * B], uint32_t row, int x, SZ sz) {
   constexpr int per = 32 / B, pairs = per / 2;
 #pragma unroll
@@ -356,7 +387,8 @@ __device__ __forceinline__ void expand_row(const uint32_t (&w)[2 * B], uint32_t 
     for (int i = 0; i < pairs; ++i) {
       uint32_t s2, z2;
       sz(j, j * pairs + i, s2, z2);
-      h[i] = bits2(__hfma2(code_pair<B>(w[j], w8, i), half2_of(s2), half2_of(z2)));
+      const __half2 y = __hfma2(code_pair<B>(w[j], w8, i), half2_of(s2), half2_of(z2));
+      h[i] = bits2(LIMIT ? limit2(y) : y);
     }
     if constexpr (NATURAL && B != 8) {
       uint32_t o[pairs];
@@ -457,14 +489,6 @@ __device__ bool copy_parts(const ChunkParams& p, const Item& it, uint32_t smem, 
   return true;
 }
 
-__device__ __forceinline__ uint4 lds16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
 __device__ __forceinline__ uint32_t lds4(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -545,17 +569,18 @@ __device__ bool produce_keys(const ChunkParams& p, const Item& it, uint32_t smem
     if (valid <= 0) {
       zero_row(row);
     } else if (axis0) {
-      expand_row<KB, false>(w, row, kt & 7, [&](int, int pair, uint32_t& s2, uint32_t& z2) {
+      expand_row<KB, false, false>(w, row, kt & 7, [&](int, int pair, uint32_t& s2, uint32_t& z2) {
         s2 = s[pair >> 4];
         z2 = z[pair >> 4];
       });
+      if (past_fp16<KB>(s, z)) limit_row(row);
     } else {
       // per-token keys: the (scale, zero) of each token, the same for a group's
       // channels (a second block that is not there leaves what the stage held:
       // its tokens are hidden)
       constexpr int per = 32 / KB;
       uint32_t t[per];
-      expand_row<KB, false>(w, row, kt & 7, [&](int word, int pair, uint32_t& s2, uint32_t& z2) {
+      expand_row<KB, false, true>(w, row, kt & 7, [&](int word, int pair, uint32_t& s2, uint32_t& z2) {
         const int i = pair % (per / 2);
         if (i == 0) {
           const uint32_t at = src + (word < KB ? tok + word * per * 4 * ng : tok2 + (word - KB) * per * 4 * ng);
@@ -655,10 +680,11 @@ __device__ bool produce_values(const ChunkParams& p, const Item& it, uint32_t sm
     if (valid <= 0) {
       zero_row(row);
     } else {
-      expand_row<VB, true>(w, row, place & 7, [&](int, int pair, uint32_t& s2, uint32_t& z2) {
+      expand_row<VB, true, false>(w, row, place & 7, [&](int, int pair, uint32_t& s2, uint32_t& z2) {
         s2 = s[pair >> 4];
         z2 = z[pair >> 4];
       });
+      if (past_fp16<VB>(s, z)) limit_row(row);
     }
     if (u & 1) {
       fence_async_smem();

@@ -355,6 +355,8 @@ KVQ_API kvq_status kvq_decode_step(kvq_cache* cache, int32_t layer, const void* 
  * The tensor-core kernel rounds dequantized keys and values to fp16 (once,
  * from q*d + m) and probabilities to the type of the values they multiply;
  * scores, softmax statistics and outputs are accumulated in fp32. A
+ * dequantized key or value above 65504, the largest finite fp16 number (a
+ * group's scale rounded up; bf16 tokens that large), is taken as 65504. A
  * non-finite key or value makes every query row that shares its 128-token
  * tile undefined, whether the row sees it or not.                          */
 KVQ_API kvq_status kvq_chunk_attention(kvq_cache* cache, int32_t layer, const void* k, const void* v, const void* q,
@@ -393,7 +395,8 @@ KVQ_API kvq_status kvq_decode_step_window(kvq_cache* cache, int32_t layer, const
  *   kvq_decode_attention and kvq_decode_step read pages that three or more
  *   neighbouring sequences of the batch share once for all of them, where
  *   that is faster (long prompts or many copies); the result is the same up
- *   to the order of fp32 sums and the roundings kvq_chunk_attention states.
+ *   to the order of fp32 sums and the roundings (and the limit to 65504) that
+ *   kvq_chunk_attention states.
  * No counterpart on the pages: the cache side of parallel sampling.         */
 KVQ_API kvq_status kvq_fork_sequence(kvq_cache* cache, int32_t src, const int32_t* dsts, int32_t num_dsts,
                                      void* stream);
