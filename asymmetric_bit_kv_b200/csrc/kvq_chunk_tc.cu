@@ -21,8 +21,9 @@
 // Warps: 0-3 and 4-7 the softmax of slots 0 and 1 (a thread owns a row, so
 // maxima, sums and the rotation of a row need no exchange), 8, 9, 12, 13 key
 // tiles, 10, 11, 14, 15 value tiles (each kind on two of the four schedulers),
-// 16 issues the MMAs, 17 copies packed parts (18, 19 idle: registers move between
-// whole warpgroups, setmaxnreg 144 + 144 + 72 + 72 + 48 = 5 x 96). The hot
+// 16 issues the MMAs, 17 copies packed parts, 18 and 19 look through the values
+// of tiles that some rows see in part (registers move between whole warpgroups,
+// setmaxnreg 144 + 144 + 72 + 72 + 48 = 5 x 96). The hot
 // loops are kept short (half a row of scores, one row of codes at a time) and
 // what runs once per item is kept rolled: four roles share an SM's instruction
 // caches, and unrolled whole tiles spent most of their time waiting for
@@ -78,11 +79,11 @@ constexpr int kTileBytes = kTile * kD * 2;
 constexpr int kHalf = kTileBytes / 2;  // one 64-wide block of a tile: 128 rows of 128 bytes
 constexpr int kQOff = 0, kKOff = 2 * kTileBytes, kVOff = kKOff + kKStages * kTileBytes;
 constexpr int kBarOff = kVOff + kVStages * kTileBytes;
-constexpr int kBarBytes = 8 * (2 * kKStages + 2 * kVStages + 4 * 2 + 2 * kRawStages + 1);
+constexpr int kBarBytes = 8 * (2 * kKStages + 3 * kVStages + 4 * 2 + 3 * kRawStages + 1);
 constexpr int kRawOff = kBarOff + 256, kRawBytes = 34304;  // packed parts: at most 18,432 bytes each
 constexpr int kSmemBytes = kRawOff + kRawBytes + 1024;     // + alignment of the base to 1024
 static_assert(kBarBytes <= 8 * 32 && kBarBytes <= kRawOff - kBarOff, "a barrier per lane of a warp");
-static_assert(kSmemBytes + 128 <= 227 * 1024, "shared memory of one CTA");
+constexpr int kMixed = 10;  // tiles of an item that some of its rows see in part (Lost)
 constexpr int kTmemS = 0, kTmemO = 256;           // columns of slot 0; slot 1 is 128 further
 constexpr float kOffset = 6.f, kMost = 16384.f;  // of the probabilities: see above
 constexpr long long kWaitCycles = 4000000000LL;
@@ -417,7 +418,45 @@ __device__ __forceinline__ void zero_row(uint32_t row) {
 
 struct Bars {  // shared-memory addresses of arrays of barriers
   uint32_t k_full, k_empty, v_full, v_empty, s_full, p_ready, o_done, q_ready, raw_full, raw_empty, drain;
+  uint32_t v_look, raw_look;  // in the place of v_full, raw_full for a mixed tile (Lost)
 };
+
+// What a row does not see must not matter, but 0 times an infinite or NaN value
+// is NaN. In a mixed tile, which some of the item's rows see in part only, such
+// values are therefore taken as zeros, and their tokens noted, a bit each: the
+// rows that see one become NaN in the end (lose_row). Mixed tiles are a window's
+// first ones of phase A (its low edge moves over at most 255 tokens, 3 tiles), the
+// sinks' and a window's first ones of phase B, and the last ones, where each row
+// sees up to its own token. A tile that all rows see needs none of this. Warps 18
+// and 19 look through mixed tiles between their arrival and their use, so that
+// the others' loops stay as they are: 4096 new tokens over 32768 take 2610 us (2570
+// without all of this), 16 x 5 over 8192 126 (119). In the value warps' loop, by
+// calls that hardly ever ran, it cost 2630 to 2800 and 130 to 143.
+struct Lost {
+  uint32_t bits[4 * kMixed];
+  int any;
+  int a_end, b_low, b_high, end;  // mixed: tiles k < a_end of phase A, k < b_low and k >= b_high of phase B, k < end
+
+  __device__ __forceinline__ void set(const ChunkParams& p, const Item& it) {
+    const int low_a = p.window > 0 ? it.q + it.n + it.t1 - p.window : -1;  // hidden from some row: up to here
+    const int low_b = p.window > 0 ? it.s + it.n + it.t1 - p.window : -1;
+    a_end = low_a < 0 ? 0 : min(it.nA, low_a / kTile - it.a0 + 1);
+    b_low = it.nA + (low_b < 0 ? 0 : it.b_sink + max(0, low_b / kTile - it.b0 + 1));
+    b_high = it.nA + max(0, (it.s + it.n + it.t0 + 1) / kTile - it.b0 + it.b_sink);
+    end = it.nA + it.nB;
+    any = 0;
+  }
+  // Number of tile k among the mixed ones, or -1.
+  __device__ __forceinline__ int tile_a(int k) const { return k < a_end ? k : -1; }
+  __device__ __forceinline__ int tile_b(int k, int nA) const {
+    return k < b_low ? 3 + k - nA : k >= b_high ? 6 + end - k : -1;
+  }
+  __device__ __forceinline__ void note(int tile, int token) {
+    atomicOr(&bits[4 * tile + (token >> 5)], 1u << (token & 31));
+    *reinterpret_cast<volatile int*>(&any) = 1;
+  }
+};
+static_assert(kSmemBytes + sizeof(Lost) + 16 <= 227 * 1024, "shared memory of one CTA");
 
 // Packed parts. Warp 17 copies every 64-token part of the item's quantized
 // tiles (one block, a tile of a 128-token block with the block's key scales, or
@@ -452,19 +491,21 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const uint8_t* src, uint3
                : "memory");
 }
 // One thread.
-__device__ bool copy_parts(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, volatile int* abort) {
+__device__ bool copy_parts(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, const Lost& lost,
+                           volatile int* abort) {
   const LayerView& L = p.L;
   const int tiles = min(it.k1, it.nA) - it.k0;
   const RawLayout raw(L);
   RawRing ring(raw.stages);
-  const int G = L.group_k;
+  const int G = L.group_k, mixed = 2 * (lost.a_end - it.k0);  // parts of mixed tiles, which come first
+  auto arrived = [&](int u) { return (u < mixed ? bar.raw_look : bar.raw_full) + 8 * (u % raw.stages); };
   for (int u = 0; u < 2 * tiles; ++u, ring.next()) {
     const int pos = (it.a0 + it.k0) * kTile + 64 * u;
     if (u >= raw.stages && !mbar_wait(bar.raw_empty + 8 * ring.stage, ring.parity ^ 1u, abort)) {
-      for (int v = u - raw.stages; v < u; ++v) mbar_drain(bar.raw_full + 8 * (v % raw.stages), (v / raw.stages) & 1);
+      for (int v = u - raw.stages; v < u; ++v) mbar_drain(arrived(v), (v / raw.stages) & 1);
       return false;
     }
-    const uint32_t full = bar.raw_full + 8 * ring.stage, dst = smem + kRawOff + ring.stage * raw.bytes;
+    const uint32_t full = arrived(u), dst = smem + kRawOff + ring.stage * raw.bytes;
     if (pos >= it.q) {
       mbar_arrive(full);
       continue;
@@ -485,7 +526,7 @@ __device__ bool copy_parts(const ChunkParams& p, const Item& it, uint32_t smem, 
   }
   // (as in produce_exact: after an abort nobody else may wait for the last ones)
   for (int v = max(0, 2 * tiles - raw.stages); v < 2 * tiles; ++v)
-    mbar_drain(bar.raw_full + 8 * (v % raw.stages), (v / raw.stages) & 1);
+    mbar_drain(arrived(v), (v / raw.stages) & 1);
   return true;
 }
 
@@ -703,8 +744,10 @@ __device__ bool produce_values(const ChunkParams& p, const Item& it, uint32_t sm
 // operands take [64-channel half][token][128 bytes]). A tile of new tokens
 // only is one TMA load per half; the others (sinks, ring, the chunk's end) are
 // copied row by row, with zeros past the last token that a row sees.
+// lost: of values, whose mixed tiles arrive at `look`; else null.
 template <int STAGES>
 __device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t tiles, uint32_t full, uint32_t empty,
+                              const Lost* lost, uint32_t look,
                               const void* sink, const void* ring, const void* fresh, const CUtensorMap* map, int kt,
                               volatile int* abort) {
   const LayerView& L = p.L;
@@ -716,13 +759,21 @@ __device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t til
   const int64_t stride = (int64_t)L.num_kv_heads * 16;
   const int held = it.s + it.n, last = held + it.t1;
   const int slot0 = it.q % L.residual;  // ring slot of the first ring token
+  uint32_t looks = 0;                   // bit st: parity of the mixed tiles so far in stage st
+  auto tile_mbar_drain = [&](int n) {   // of the item's tile n, the last one in its stage
+    const int k = it.k0 + n, st = n % STAGES;
+    if (lost && k >= it.nA && lost->tile_b(k, it.nA) >= 0) mbar_drain(look + 8 * st, ((looks >> st) & 1u) ^ 1u);
+    else mbar_drain(full + 8 * st, (n / STAGES) & 1);
+  };
   for (int k = max(it.k0, it.nA); k < it.k1; ++k) {
     const int c = k - it.k0, st = c % STAGES, e0 = it.tile_b(k) * kTile;
     if (c >= STAGES && !mbar_wait_warp(empty + 8 * st, ((c / STAGES) - 1) & 1, abort)) {
-      for (int v = c - STAGES; v < c; ++v) mbar_drain(full + 8 * (v % STAGES), (v / STAGES) & 1);
+      for (int n = c - STAGES; n < c; ++n) tile_mbar_drain(n);
       return false;
     }
-    const uint32_t dst = tiles + st * kTileBytes, bar = full + 8 * st;
+    const bool mixed = lost && lost->tile_b(k, it.nA) >= 0;
+    if (mixed) looks ^= 1u << st;
+    const uint32_t dst = tiles + st * kTileBytes, bar = (mixed ? look : full) + 8 * st;
     if (e0 >= held && e0 - held + kTile <= p.e[it.i].t) {
       if ((kt & 31) == 0) {
         if (kt == 0) {
@@ -763,8 +814,81 @@ __device__ bool produce_exact(const ChunkParams& p, const Item& it, uint32_t til
   // the last copies, in case of an abort: the block must not end under them
   // (else they have been waited for by the time that the others end)
   if (kt == 0)
-    for (int c = max(max(it.k0, it.nA), it.k1 - STAGES) - it.k0; c < it.k1 - it.k0; ++c)
-      mbar_drain(full + 8 * (c % STAGES), (c / STAGES) & 1);
+    for (int n = max(max(it.k0, it.nA), it.k1 - STAGES) - it.k0; n < it.k1 - it.k0; ++n) tile_mbar_drain(n);
+  return true;
+}
+
+// Warps 18 and 19 (x: thread of 64): the values of mixed tiles. Of a part of phase
+// A (warp 18: whoever waits for a stage's phases must wait for each) the scales
+// and zero points of tokens that are not finite become 0, before the value warps
+// expand them; in a tile of phase B 16-byte pieces with values that are not finite
+// do.
+__device__ bool look_through(const ChunkParams& p, const Item& it, uint32_t smem, const Bars& bar, int x, Lost& lost,
+                             volatile int* abort) {
+  const LayerView& L = p.L;
+  const int parts = 2 * (min(min(it.k1, it.nA), lost.a_end) - it.k0);
+  if (x < 32 && parts > 0) {
+    const RawLayout raw(L);
+    RawRing ring(raw.stages);
+    const int TT = L.tile_tokens, ng = kD / L.group_v;
+    const bool order = vsz_operand_order(TT, L.k_bits);
+    const int zero = order ? 8 : 2, next = order ? 16 : 4;  // bytes from a scale to its zero point, to the next group's
+    uint32_t at[2];  // the first scale of tokens x and x + 32
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      at[e] = smem + kRawOff + raw.tile + L.vsz_off + (TT == 32 ? e * (int)L.record_bytes : 0) +
+              2 * vsz_half_index(TT == 32 ? x : x + 32 * e, 0, TT, L.k_bits, ng, false);
+#pragma unroll 1
+    for (int u = 0; u < parts; ++u, ring.next()) {
+      if (!mbar_wait_warp(bar.raw_look + 8 * ring.stage, ring.parity, abort)) return false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if ((it.a0 + it.k0) * kTile + 64 * u + x + 32 * e >= it.q) break;
+        const uint32_t first = at[e] + ring.stage * raw.bytes;
+        bool finite = true;
+#pragma unroll 1
+        for (uint32_t sz = first; sz < first + ng * next; sz += next) {
+          if ((lds2(sz) & 0x7c00u) != 0x7c00u && (lds2(sz + zero) & 0x7c00u) != 0x7c00u) continue;
+          asm volatile("st.shared.u16 [%0], %2;\n st.shared.u16 [%1], %2;" ::"r"(sz), "r"(sz + zero),
+                       "h"((unsigned short)0)
+                       : "memory");
+          finite = false;
+        }
+        if (!finite) lost.note(lost.tile_a(it.k0 + (u >> 1)), 64 * (u & 1) + x + 32 * e);
+      }
+      fence_async_smem();  // (the stage is copied into again)
+      __syncwarp();
+      if (x == 0) mbar_arrive(bar.raw_full + 8 * ring.stage);
+    }
+  }
+  // exponents of ones only carry into the sign bits
+  const uint32_t one = L.kv_dtype == KVQ_BF16 ? 0x00800080u : 0x04000400u, exponents = 0x80008000u - one;
+  uint32_t looks = 0;
+#pragma unroll 1
+  for (int k = max(it.k0, it.nA); k < it.k1; ++k) {
+    const int tile = lost.tile_b(k, it.nA), st = (k - it.k0) % kVStages;
+    if (tile < 0) continue;
+    if (!mbar_wait_warp(bar.v_look + 8 * st, (looks >> st) & 1u, abort)) return false;
+    looks ^= 1u << st;
+    // (tokens past the item's last row too: a tile copied as a whole has them)
+    const int rows = min(kTile, it.s + it.n + p.e[it.i].t - it.tile_b(k) * kTile);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      const uint32_t first = smem + kVOff + st * kTileBytes + half * kHalf + (x & 7) * 16;
+#pragma unroll 4
+      for (int row = x >> 3; row < rows; row += 8) {
+        const uint4 v = lds16(first + row * 128);
+        const uint32_t a = ((v.x & exponents) + one) | ((v.y & exponents) + one);
+        const uint32_t b = ((v.z & exponents) + one) | ((v.w & exponents) + one);
+        if (((a | b) & 0x80008000u) == 0u) continue;
+        sts16(first + row * 128, 0u, 0u, 0u, 0u);
+        lost.note(tile, row);
+      }
+    }
+    fence_async_smem();
+    __syncwarp();
+    if ((x & 31) < kProducers / 64) mbar_arrive(bar.v_full + 8 * st);  // for the four value warps
+  }
   return true;
 }
 
@@ -1251,11 +1375,46 @@ __device__ bool issue_products(const ChunkParams& p, const Item& it, uint32_t sm
   return true;
 }
 
+// After all else, where values were left out: thread x of 256 makes its row NaN
+// (its output, or the sum of its part) if it sees one of them.
+// (The softmax has all that this works out again, and no registers to keep it:
+// there it cost 16 x 5 tokens over 8192 15 us.)
+__device__ __forceinline__ void lose_row(const ChunkParams& p, const Lost& lost, int x) {
+  const Item it = find_item(p, blockIdx.x);
+  const int w = x >> 7, r = it.r0 + (it.both ? x : x & 127);
+  if (r >= it.rows) return;
+  const int t = r >> it.lg, hi_b = it.s + it.n + t, sinks = min(it.first_e, hi_b + 1);
+  const int lo_a = p.window > 0 ? it.q + it.n + t - p.window : -1, lo_b = p.window > 0 ? hi_b - p.window : -1;
+  bool sees = false;
+  for (int k = it.k0; k < it.k1 && !sees; ++k) {
+    const bool in_a = k < it.nA;
+    const int tile = in_a ? lost.tile_a(k) : lost.tile_b(k, it.nA);
+    for (int e = 0; e < 4 && tile >= 0; ++e) {
+      const int c = (in_a ? it.a0 + k : it.tile_b(k)) * kTile + 32 * e;
+      const uint32_t seen = in_a ? bit_range(lo_a + 1 - c, it.q - c)
+                                 : bit_range(lo_b + 1 - c, hi_b + 1 - c) | bit_range(0 - c, sinks - c);
+      sees = sees || (lost.bits[4 * tile + e] & seen) != 0u;
+    }
+  }
+  if (!sees) return;
+  const float nan = __int_as_float(0x7fffffff);
+  if (it.parts > 1) {
+    p.ws_ml[p.e[it.i].part0 + it.part + (it.both ? 0 : w) + ((int64_t)it.h * it.rows + r) * it.parts].y = nan;
+    return;
+  }
+  const int64_t at = it.row_of(p, r) * kD;
+  for (int c = 0; c < kD; ++c) {
+    if (p.out_dtype == KVQ_F32) static_cast<float*>(p.out)[at + c] = nan;
+    else static_cast<uint16_t*>(p.out)[at + c] = 0x7fffu;  // NaN in both types
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ ChunkMaps maps) {
   extern __shared__ uint8_t raw[];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ Lost s_lost;
   const uint32_t smem = (smem_u32(raw) + 1023u) & ~1023u;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   volatile int* abort = &s_abort;
@@ -1272,6 +1431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bar.q_ready = at, at += 16;
     bar.raw_full = at, at += 8 * kRawStages;
     bar.raw_empty = at, at += 8 * kRawStages;
+    bar.raw_look = at, at += 8 * kRawStages;
+    bar.v_look = at, at += 8 * kVStages;
     bar.drain = at;
   }
   // the merge of the parts may be scheduled (it waits for this grid before it
@@ -1283,10 +1444,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t at = smem + kBarOff + 8 * lane;
     auto in = [&](uint32_t first, int n) { return at >= first && at < first + 8 * n; };
     // arrivals: of the key or value warps, of a slot's warps, of one thread or a commit
-    const bool produced = in(bar.k_full, kKStages) || in(bar.v_full, kVStages);
+    const bool produced = in(bar.k_full, kKStages) || in(bar.v_full, kVStages) || in(bar.v_look, kVStages);
     const bool slot = in(bar.p_ready, 2) || in(bar.q_ready, 2), raw_empty = in(bar.raw_empty, kRawStages);
     if (8 * lane < kBarBytes) mbar_init(at, produced ? kProducers / 32 : slot ? 4 : raw_empty ? kProducers / 16 : 1);
-    if (lane == 0) s_abort = 0;
+    if (lane == 0) {
+      s_abort = 0;
+      s_lost.set(p, it);
+    }
+    for (int e = lane; e < 4 * kMixed; e += 32) s_lost.bits[e] = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 16) {
@@ -1313,15 +1478,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                       : L.k_bits == 4 ? produce_keys<4>(p, it, smem, bar, kt, abort)
                                       : produce_keys<8>(p, it, smem, bar, kt, abort);
       if (ok)
-        (void)produce_exact<kKStages>(p, it, smem + kKOff, bar.k_full, bar.k_empty, L.sink_k, L.ring_k, p.k, &maps.k,
-                                      kt, abort);
+        (void)produce_exact<kKStages>(p, it, smem + kKOff, bar.k_full, bar.k_empty, nullptr, 0u, L.sink_k, L.ring_k, p.k,
+                                      &maps.k, kt, abort);
     } else {
       const bool ok = L.v_bits == 2   ? produce_values<2>(p, it, smem, bar, kt, abort)
                       : L.v_bits == 4 ? produce_values<4>(p, it, smem, bar, kt, abort)
                                       : produce_values<8>(p, it, smem, bar, kt, abort);
       if (ok)
-        (void)produce_exact<kVStages>(p, it, smem + kVOff, bar.v_full, bar.v_empty, L.sink_v, L.ring_v, p.v, &maps.v,
-                                      kt, abort);
+        (void)produce_exact<kVStages>(p, it, smem + kVOff, bar.v_full, bar.v_empty, &s_lost, bar.v_look, L.sink_v, L.ring_v,
+                                      p.v, &maps.v, kt, abort);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
@@ -1334,7 +1499,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_drain(bar.drain, 0);
       __syncwarp();
     }
-    if (warp == 17 && (threadIdx.x & 31) == 0) (void)copy_parts(p, it, smem, bar, abort);
+    if (warp == 17 && (threadIdx.x & 31) == 0) (void)copy_parts(p, it, smem, bar, s_lost, abort);
+    if (warp >= 18) (void)look_through(p, it, smem, bar, threadIdx.x & 63, s_lost, abort);
     __syncwarp();
   }
   tc_before();
@@ -1343,6 +1509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 16)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   if (threadIdx.x == 0 && s_abort) atomicOr(p.err, 1);
+  if (s_lost.any && threadIdx.x < 2 * kRows) lose_row(p, s_lost, threadIdx.x);
 }
 
 // Merges the parts of a row (parts > 1): a warp per row, four channels a lane.

@@ -357,8 +357,8 @@ KVQ_API kvq_status kvq_decode_step(kvq_cache* cache, int32_t layer, const void* 
  * scores, softmax statistics and outputs are accumulated in fp32. A
  * dequantized key or value above 65504, the largest finite fp16 number (a
  * group's scale rounded up; bf16 tokens that large), is taken as 65504. A
- * non-finite key or value makes every query row that shares its 128-token
- * tile undefined, whether the row sees it or not.                          */
+ * key or value that is not finite reaches the query rows that see its token
+ * and no others; in those, any element may be NaN.                         */
 KVQ_API kvq_status kvq_chunk_attention(kvq_cache* cache, int32_t layer, const void* k, const void* v, const void* q,
                                        void* out, int32_t out_dtype, float softmax_scale, const int32_t* new_lens,
                                        int32_t batch, int32_t window, void* stream);

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import test_gpu_fork_decode as F
-from attention_reference import attend, cached_tokens
+from attention_reference import attend, bound, cached_tokens
 from oracle import kvq_oracle as O
 from test_gpu_chunk import FORMATS, make, tokens
 
@@ -82,4 +82,92 @@ def test_decode_of_the_largest_values_alone_and_of_copies(fmt, copies):
     k, v = cached_tokens(cache, 0, 0)
     for b in range(copies):
         assert_allowed(out[b:b + 1], attend(q[b:b + 1], k, v, k.shape[0] - 1, SCALE), cfg, f"{fmt} sequence {b} of {copies}")
+    cache.close()
+
+
+BAD = (float("nan"), float("inf"), float("-inf"))
+
+
+def check_rows(cache, k, v, q, lens, bad, window, what):
+    """bad[b]: tokens of sequence b (cached or new) whose values, and of new ones some keys, are infinite or NaN. A row
+    that sees none of them is as if they were not there; one that does is not finite."""
+    cfg = cache.cfg
+    out = cache.chunk_attention(0, k, v, q, lens, out_dtype=torch.float32, window=window)
+    off = hidden = 0
+    for b, t in enumerate(lens):
+        ck, cv = cached_tokens(cache, 0, b)
+        n = ck.shape[0]
+        kk, vv = torch.cat([ck, k[off:off + t].double()]), torch.cat([cv, v[off:off + t].double()])
+        kk[bad[b]], vv[bad[b]] = 0.0, 0.0
+        assert torch.isfinite(kk).all() and torch.isfinite(vv).all()
+        i, j = torch.arange(n, n + t, device="cuda")[:, None], torch.tensor(bad[b], device="cuda")[None, :]
+        sees = j <= i
+        if window:
+            sees &= (j > i - window) | (j < cfg.sink_tokens)
+        sees = sees.any(1)
+        ref = attend(q[off:off + t], kk, vv, n, 128 ** -0.5, window, cfg.sink_tokens)
+        got, clean = out[off:off + t], ~sees
+        err, tol = (got.double() - ref[0]).abs(), bound(ref, 128 ** -0.5, cfg, torch.float32)
+        assert torch.isfinite(got[clean]).all(), f"{what} sequence {b}: what a row does not see reached it"
+        assert (err[clean] <= tol[clean]).all(), f"{what} sequence {b}"
+        assert not torch.isfinite(got[sees]).all(-1).any(), f"{what} sequence {b}: a row hides what it sees"
+        off += t
+        hidden += int(clean.sum())
+    assert cache.device_errors() == 0
+    return hidden
+
+
+def plant(x, at, gen):
+    for e, i in enumerate(at):
+        c = torch.randint(128, (1 + 40 * (e % 2),), generator=gen, device="cuda")
+        x[i, :, c] = BAD[e % 3]
+
+
+@pytest.mark.parametrize("window", [1, 16, 100, 129, 300])
+@pytest.mark.parametrize("fmt", sorted(FORMATS))
+def test_tokens_outside_the_window_may_hold_anything(fmt, window):
+    hidden = 0
+    for seed, lens in enumerate([[201, 300], [5, 1], [20, 33], [64, 700]]):
+        cache = make(fmt, 2)
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        held = [900, 5]
+        k, v, _ = tokens(sum(held), cache.cfg, gen)
+        S = cache.cfg.sink_tokens
+        old = [900 - x for x in (1, 2, 40, 70, 127, 130, 190, 260, 299)]
+        plant(v, old, gen)
+        cache.append(0, k, v, held)
+        k, v, q = tokens(sum(lens), cache.cfg, gen)
+        new = [x for x in (0, 3, 90, 150, 199) if x < lens[0]], [x for x in (4, 64, 127, 129, 290, 650) if x < lens[1]]
+        for x in (k, v):
+            plant(x, [*new[0], *(lens[0] + y for y in new[1])], gen)
+        bad = [old + [900 + y for y in new[0]], [5 + y for y in new[1]]]
+        assert min(bad[0]) >= S and (not bad[1] or min(bad[1]) >= S)
+        hidden += check_rows(cache, k, v, q, lens, bad, window, f"{fmt} window {window} {lens}")
+        cache.close()
+    assert hidden > 0
+
+
+@pytest.mark.parametrize("held", [0, 3, 500])
+@pytest.mark.parametrize("fmt", sorted(FORMATS))
+def test_later_tokens_may_hold_anything(fmt, held):
+    for seed, (lens, new) in enumerate([([400, 130], ([257, 300, 399], [129])), ([7, 30], ([6], [11, 12])), ([1, 1000], ([], [513, 999]))]):
+        cache = make(fmt, 2)
+        gen = torch.Generator(device="cuda").manual_seed(20 + seed)
+        k, v, _ = tokens(2 * held, cache.cfg, gen)
+        cache.append(0, k, v, [held, held])
+        k, v, q = tokens(sum(lens), cache.cfg, gen)
+        for x in (k, v):
+            plant(x, [*new[0], *(lens[0] + y for y in new[1])], gen)
+        check_rows(cache, k, v, q, lens, [[held + y for y in n] for n in new], 0, f"{fmt} {held} {lens}")
+        cache.close()
+
+
+def test_a_sink_that_is_not_finite_reaches_every_row():
+    cache = make("bq2", 1)
+    gen = torch.Generator(device="cuda").manual_seed(30)
+    k, v, _ = tokens(800, cache.cfg, gen)
+    plant(v, [2], gen)
+    cache.append(0, k, v, [800])
+    k, v, q = tokens(90, cache.cfg, gen)
+    assert check_rows(cache, k, v, q, [90], [[2]], 130, "sink") == 0
     cache.close()
