@@ -154,7 +154,17 @@ struct Plan {
   int32_t slots, max_pages;
   int64_t partials;  // rows of the split-partial workspace
 };
-constexpr int64_t kMinPartials = 32768;
+// Workspace rows that the tensor-core chunk kernel's parts need at least: a wave of
+// its items, one to each of 148 SMs, writes up to 148 x 256 rows of one part; the
+// power of two below that holds the waves whose last items are not full (17 MB).
+// Only for caches that it serves and that are long enough for two ranges of
+// kLeastTiles tiles. Measured without / with, new tokens over cached ones (32 query
+// and 8 KV heads, K2 V4), in us with 30 of launch: 100 over 8190 110 / 83, 300 over
+// 8190 210 / 120, 300 over 32000 638 / 257, 1000 over 4000 147 / 136, 300 over 2000
+// 81 / 67, 300 over 900 62 / 60; with twice as many 84, 120, 256, 135, 67, 60.
+constexpr int64_t kWaveRows = 32768;
+constexpr int64_t kLeastTiles = 4;  // tiles of a range
+static_assert(kWaveRows <= 148 * 2 * kvq::kChunkSlotRows && 2 * kWaveRows > 148 * 2 * kvq::kChunkSlotRows, "a wave");
 
 Plan make_plan(const kvq_config* c) {
   using kvq::round_up;
@@ -199,9 +209,9 @@ Plan make_plan(const kvq_config* c) {
       std::min<int64_t>(p.max_blocks, KVQ_MAX_SPLITS) + 1,
       kvq::kMmaConsumers *
           (std::min<int64_t>(p.max_blocks + (c->residual + kvq::kResChunk - 1) / kvq::kResChunk + 1, 64) + 2));
-  // (and, for chunk attention, for a few ranges of some hundred query tokens of
-  // a small cache: 300 tokens of 32 heads in 3 ranges are 28,800 rows)
-  p.partials = std::max<int64_t>((int64_t)c->max_batch * c->num_q_heads * p.slots, kMinPartials);
+  p.partials = (int64_t)c->max_batch * c->num_q_heads * p.slots;
+  if (residual_v_of(*c) == c->residual && c->max_tokens >= 2 * kLeastTiles * kvq::kChunkTile)
+    p.partials = std::max(p.partials, kWaveRows);
   p.ws_o_off = off;
   off = round_up(off + p.partials * D * 4, 256);
   p.ws_ml_off = off;
@@ -471,7 +481,7 @@ kvq_status check_window(const kvq_cache* c, int32_t window) {
 // plus the merge of the parts. (4096 tokens over 32768, 512 units on 148 SMs:
 // uncut 3.46 waves run as 4; 2 ranges each run as 7 half waves, 10% sooner.)
 kvq_status plan_chunk(const kvq_cache* c, kvq::ChunkParams& p) {
-  constexpr int64_t kItemTiles = 4, kLeast = 4, kMostRanges = 64;
+  constexpr int64_t kItemTiles = 4, kLeast = kLeastTiles, kMostRanges = 64;
   // (shared pages: half of a row's slots are the decode kernel's)
   const int64_t most_ranges = p.slots > 0 ? std::max(1, std::min<int32_t>(kMostRanges, p.slots / 4)) : kMostRanges;
   constexpr double kRecordTiles = 7e-5;  // tiles' time to write and read one part of a row

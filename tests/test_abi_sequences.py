@@ -5,7 +5,7 @@ import ctypes
 import pytest
 import torch
 
-from asymmetric_bit_kv_b200 import load_library
+from asymmetric_bit_kv_b200 import CacheConfig, load_library, required_bytes
 from asymmetric_bit_kv_b200 import kvq as K
 
 
@@ -29,3 +29,18 @@ def test_the_binding_checks_shapes_and_types():
         K.KVCache._out_like(t, None, torch.float64)
     with pytest.raises(ValueError, match="not supported"):
         K.KVCache._out_like(t, torch.zeros(2, 3, dtype=torch.int32), torch.float32)
+
+
+def test_the_workspace_of_chunk_attention_is_there_where_it_is_used():
+    """(the arena of a short cache, or of one with separate key and value windows, does not hold it)"""
+    def size(**kw):
+        base = dict(num_layers=1, max_batch=2, num_q_heads=8, num_kv_heads=2, head_dim=128, max_tokens=512, group_k=64,
+                    group_v=64, residual=128, kv_dtype=torch.bfloat16, k_bits=[2], v_bits=[4])
+        return required_bytes(CacheConfig(**{**base, **kw}))
+
+    rows = 128 * 4 + 8  # bytes of a partial row
+    assert size() < 1 << 21
+    long = size(max_tokens=4096)
+    assert long >= 32768 * rows  # a wave of items with one part a row
+    # separate windows: what decode's parts need, 16 rows x 66 x 6, in its place
+    assert size(max_tokens=4096, residual_v=64) <= long - (32768 - 16 * 66 * 6) * rows
