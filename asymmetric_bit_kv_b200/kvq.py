@@ -159,11 +159,11 @@ def _need_shape(t: torch.Tensor, shape: tuple, name):
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
 
 
-def _window(window: int) -> int:
-    """window, refused where ctypes would cut it to 32 bits without a word."""
-    if not -2 ** 31 <= window < 2 ** 31:
-        raise ValueError(f"window {window} does not fit 32 bits")
-    return window
+def _int32(x: int, name: str) -> int:
+    """x, refused where ctypes would cut it to 32 bits without a word."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} {x} does not fit 32 bits")
+    return x
 
 
 @dataclass
@@ -209,7 +209,7 @@ def required_bytes(cfg: CacheConfig) -> int:
 
 def lens_array(new_lens) -> ctypes.Array:
     """new_lens as the int32 array kvq_append takes (reusable across calls)."""
-    n = [int(x) for x in new_lens]
+    n = [_int32(int(x), "length or index") for x in new_lens]
     return (ctypes.c_int32 * len(n))(*n)
 
 
@@ -328,6 +328,7 @@ class KVCache:
         q: [sum(new_lens), Hq, D] in the cache dtype; new_lens as in append.
         window: 0, or the tokens a query sees besides the sinks. Returns out
         [sum(new_lens), Hq, D]."""
+        layer = _int32(layer, "layer")
         _need(k, self.cfg.kv_dtype, "k")
         _need(v, self.cfg.kv_dtype, "v")
         _need(q, self.cfg.kv_dtype, "q")
@@ -342,7 +343,7 @@ class KVCache:
         with self._on_device(k, v, q, out):
             _check(self.lib.kvq_chunk_attention(self.handle, layer, k.data_ptr(), v.data_ptr(), q.data_ptr(), out.data_ptr(),
                                                 _DTYPE_CODE[out.dtype], float(softmax_scale), arr, len(arr),
-                                                _window(window),
+                                                _int32(window, "window"),
                                                 _stream_ptr(stream)),
                    "kvq_chunk_attention")
         return out
@@ -351,6 +352,7 @@ class KVCache:
                                 out_dtype=torch.float32, softmax_scale: float | None = None, stream=None):
         """decode_attention over the last `window` tokens and the sinks of every
         sequence (kvq_decode_attention_window). q: [batch, Hq, D]."""
+        layer = _int32(layer, "layer")
         _need(q, self.cfg.kv_dtype, "q")
         _need_shape(q, (q.shape[0], self.cfg.num_q_heads, self.cfg.head_dim), "q")
         out = self._out_like(q, out, out_dtype)
@@ -359,7 +361,7 @@ class KVCache:
         with self._on_device(q, out):
             _check(self.lib.kvq_decode_attention_window(self.handle, layer, q.data_ptr(), out.data_ptr(),
                                                         _DTYPE_CODE[out.dtype], float(softmax_scale), q.shape[0],
-                                                        _window(window), _stream_ptr(stream)),
+                                                        _int32(window, "window"), _stream_ptr(stream)),
                    "kvq_decode_attention_window")
         return out
 
@@ -368,6 +370,7 @@ class KVCache:
                            softmax_scale: float | None = None, stream=None):
         """decode_step over the last `window` tokens and the sinks
         (kvq_decode_step_window). k, v: [batch, Hkv, D], q: [batch, Hq, D]."""
+        layer = _int32(layer, "layer")
         cfg = self.cfg
         for t, h, name in ((k, cfg.num_kv_heads, "k"), (v, cfg.num_kv_heads, "v"), (q, cfg.num_q_heads, "q")):
             _need(t, cfg.kv_dtype, name)
@@ -378,14 +381,14 @@ class KVCache:
         with self._on_device(k, v, q, out):
             _check(self.lib.kvq_decode_step_window(self.handle, layer, k.data_ptr(), v.data_ptr(), q.data_ptr(),
                                                    out.data_ptr(), _DTYPE_CODE[out.dtype], float(softmax_scale), q.shape[0],
-                                                   _window(window), _stream_ptr(stream)),
+                                                   _int32(window, "window"), _stream_ptr(stream)),
                    "kvq_decode_step_window")
         return out
 
     def fork_sequence(self, src: int, dsts, stream=None):
         """Make every sequence of dsts a copy of sequence src in all layers; a
         paged cache shares the filled pages (kvq_fork_sequence)."""
-        arr = lens_array(dsts)
+        src, arr = _int32(src, "src"), lens_array(dsts)
         with self._on_device():
             _check(self.lib.kvq_fork_sequence(self.handle, src, arr, len(arr), _stream_ptr(stream)), "kvq_fork_sequence")
 

@@ -44,3 +44,27 @@ def test_the_workspace_of_chunk_attention_is_there_where_it_is_used():
     assert long >= 32768 * rows  # a wave of items with one part a row
     # separate windows: what decode's parts need, 16 rows x 66 x 6, in its place
     assert size(max_tokens=4096, residual_v=64) <= long - (32768 - 16 * 66 * 6) * rows
+
+
+def test_integers_wider_than_32_bits_are_refused():
+    """(not cut to their low 32 bits: a copy would go to another sequence)"""
+    for bad in (2 ** 32 + 1, 2 ** 31, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="32 bits"):
+            K.lens_array([3, bad])
+    assert list(K.lens_array([3, 2 ** 31 - 1, -2 ** 31])) == [3, 2 ** 31 - 1, -2 ** 31]
+
+    class Calls:
+        def __getattr__(self, name):
+            raise AssertionError(f"{name} was called")
+
+    cache = K.KVCache.__new__(K.KVCache)
+    cache.lib, cache.handle = Calls(), None
+    with pytest.raises(ValueError, match="src .* 32 bits"):
+        cache.fork_sequence(2 ** 32, [1])
+    with pytest.raises(ValueError, match="32 bits"):
+        cache.fork_sequence(0, [1, 2 ** 32 + 2])
+    for call in (cache.chunk_attention, cache.decode_attention_window, cache.decode_step_window):
+        args = {cache.chunk_attention: (None, None, None, [1]), cache.decode_attention_window: (None, 5),
+                cache.decode_step_window: (None, None, None, 5)}[call]
+        with pytest.raises(ValueError, match="layer .* 32 bits"):
+            call(2 ** 32, *args)
