@@ -639,69 +639,105 @@ bool plan_shared(const kvq_cache* c, int layer, int batch, int32_t slot_cap, kvq
   return true;
 }
 
-// kvq_fork_sequence after its argument checks.
-kvq_status enqueue_fork(kvq_cache* c, int src, const int32_t* dsts, int nd, cudaStream_t stream) {
-  const kvq_config& cfg = c->cfg;
-  const int P = cfg.page_blocks, G = cfg.group_k;
-  if (P > 0) {
-    // let go of the destinations' pages layer by layer, counting what returns
-    // to each pool; a pool that stays short undoes all of it
-    auto row_of = [&](int l, int d) { return &c->pt_host[((size_t)l * cfg.max_batch + d) * c->max_pages]; };
+// What kvq_fork_sequence does to the page pools, worked out before the copy is
+// enqueued and carried out after it: until then only reference counts have been
+// lowered, and undo() raises them again.
+struct ForkPages {
+  std::vector<int32_t> freed;   // pages that only destinations held, layer by layer
+  std::vector<size_t> freed_at;  // [layers + 1]: where each layer's begin
+  std::vector<int32_t> tails;   // [layers][destinations]: each one's last, partly filled page (or -1)
+
+  static int blocks(const kvq_cache* c, int l, int src) {
+    const size_t i = (size_t)l * c->cfg.max_batch + src;
+    return std::max(c->q_len[i], c->qv_len[i]) / c->cfg.group_k;
+  }
+  static int32_t* row_of(kvq_cache* c, int l, int b) {
+    return &c->pt_host[((size_t)l * c->cfg.max_batch + b) * c->max_pages];
+  }
+  static int32_t* refs_of(kvq_cache* c, int l) { return &c->page_refs[(size_t)l * c->cfg.pool_pages]; }
+
+  // Room for everything below (may throw).
+  void reserve(const kvq_cache* c, const int32_t* dsts, int nd) {
+    size_t held = 0;
+    for (int l = 0; l < c->cfg.num_layers; ++l)
+      for (int i = 0; i < nd; ++i) held += c->pages_held[(size_t)l * c->cfg.max_batch + dsts[i]];
+    freed.reserve(held);
+    freed_at.reserve(c->cfg.num_layers + 1);
+    tails.reserve((size_t)c->cfg.num_layers * nd);
+    freed.clear();
+    freed_at.clear();
+    tails.clear();
+  }
+  // Lets go of the destinations' pages layer by layer and chooses their last
+  // pages, as the pools will give them; a pool that stays short undoes it all.
+  kvq_status plan(kvq_cache* c, int src, const int32_t* dsts, int nd) {
+    const kvq_config& cfg = c->cfg;
+    freed_at.push_back(0);
     for (int l = 0; l < cfg.num_layers; ++l) {
-      const size_t base = (size_t)l * cfg.max_batch;
-      int32_t* refs = &c->page_refs[(size_t)l * cfg.pool_pages];
-      int64_t have = (int64_t)c->free_pages[l].size();
+      int32_t* refs = refs_of(c, l);
       for (int i = 0; i < nd; ++i)
-        for (int k = 0; k < c->pages_held[base + dsts[i]]; ++k)
-          if (--refs[row_of(l, dsts[i])[k]] == 0) ++have;
-      const int blocks = std::max(c->q_len[base + src], c->qv_len[base + src]) / G;
-      if (blocks % P != 0 && have < nd) {
-        for (int u = 0; u <= l; ++u)
-          for (int i = 0; i < nd; ++i)
-            for (int k = 0; k < c->pages_held[(size_t)u * cfg.max_batch + dsts[i]]; ++k)
-              ++c->page_refs[(size_t)u * cfg.pool_pages + row_of(u, dsts[i])[k]];
-        return fail(KVQ_ERR_CAPACITY, "layer %d: the fork needs %d pages; the pool would have %lld free of %d", l, nd,
-                    (long long)have, cfg.pool_pages);
+        for (int k = 0; k < c->pages_held[(size_t)l * cfg.max_batch + dsts[i]]; ++k)
+          if (--refs[row_of(c, l, dsts[i])[k]] == 0) freed.push_back(row_of(c, l, dsts[i])[k]);
+      freed_at.push_back(freed.size());
+      const size_t own = freed.size() - freed_at[l], have = own + c->free_pages[l].size();
+      const bool tail = blocks(c, l, src) % cfg.page_blocks != 0;
+      if (tail && have < (size_t)nd) {
+        undo(c, dsts, nd);
+        return fail(KVQ_ERR_CAPACITY, "layer %d: the fork needs %d pages; the pool would have %zu free of %d", l, nd, have,
+                    cfg.pool_pages);
       }
+      for (size_t i = 0; i < (size_t)nd; ++i)
+        tails.push_back(!tail ? -1 : i < own ? freed[freed.size() - 1 - i] : c->free_pages[l][have - 1 - i]);
     }
+    return KVQ_OK;
+  }
+  void undo(kvq_cache* c, const int32_t* dsts, int nd) const {
+    for (int l = 0; l + 1 < (int)freed_at.size(); ++l)
+      for (int i = 0; i < nd; ++i)
+        for (int k = 0; k < c->pages_held[(size_t)l * c->cfg.max_batch + dsts[i]]; ++k)
+          ++refs_of(c, l)[row_of(c, l, dsts[i])[k]];
+  }
+  void commit(kvq_cache* c, int src, const int32_t* dsts, int nd) const {
+    const kvq_config& cfg = c->cfg;
     for (int l = 0; l < cfg.num_layers; ++l) {
-      const size_t base = (size_t)l * cfg.max_batch;
-      int32_t* refs = &c->page_refs[(size_t)l * cfg.pool_pages];
-      for (int i = 0; i < nd; ++i) {  // the counts are down already: a page at zero returns once
-        const int32_t* row = row_of(l, dsts[i]);
-        for (int k = c->pages_held[base + dsts[i]] - 1; k >= 0; --k)
-          if (refs[row[k]] == 0) {
-            refs[row[k]] = -1;
-            c->free_pages[l].push_back(row[k]);
-          }
-        c->pages_held[base + dsts[i]] = 0;
-      }
-      const int blocks = std::max(c->q_len[base + src], c->qv_len[base + src]) / G;
-      const int full = blocks / P, held = (blocks + P - 1) / P;
-      const int32_t* from = row_of(l, src);
+      int32_t* refs = refs_of(c, l);
+      std::vector<int32_t>& pool = c->free_pages[l];
+      pool.insert(pool.end(), freed.begin() + freed_at[l], freed.begin() + freed_at[l + 1]);  // (has room for all pages)
+      const int full = blocks(c, l, src) / cfg.page_blocks;
+      const int32_t* from = row_of(c, l, src);
       for (int i = 0; i < nd; ++i) {
-        int32_t* row = row_of(l, dsts[i]);
+        int32_t* row = row_of(c, l, dsts[i]);
         for (int k = 0; k < full; ++k) {
           row[k] = from[k];
           ++refs[from[k]];
         }
-        if (held > full) {
-          row[full] = c->free_pages[l].back();
-          c->free_pages[l].pop_back();
-          refs[row[full]] = 1;
+        const int32_t tail = tails[(size_t)l * nd + i];
+        if (tail >= 0) {
+          pool.pop_back();  // that one: plan() took them in this order
+          row[full] = tail;
+          refs[tail] = 1;
         }
-        c->pages_held[base + dsts[i]] = held;
+        c->pages_held[(size_t)l * cfg.max_batch + dsts[i]] = full + (tail >= 0 ? 1 : 0);
       }
     }
   }
-  for (int l = 0; l < cfg.num_layers; ++l) {
-    const size_t base = (size_t)l * cfg.max_batch;
-    for (int i = 0; i < nd; ++i) {
-      c->q_len[base + dsts[i]] = c->q_len[base + src];
-      c->n_len[base + dsts[i]] = c->n_len[base + src];
-      c->s_len[base + dsts[i]] = c->s_len[base + src];
-      c->qv_len[base + dsts[i]] = c->qv_len[base + src];
+};
+
+// kvq_fork_sequence after its argument checks. The host's mirror of the lengths
+// and pages follows the copy's first launch, so that a launch that fails leaves
+// the cache as it was.
+kvq_status enqueue_fork(kvq_cache* c, int src, const int32_t* dsts, int nd, cudaStream_t stream) {
+  const kvq_config& cfg = c->cfg;
+  const int P = cfg.page_blocks, G = cfg.group_k;
+  thread_local ForkPages pages;
+  if (P > 0) {
+    try {
+      pages.reserve(c, dsts, nd);
+    } catch (const std::bad_alloc&) {
+      return fail(KVQ_ERR_INVALID_ARG, "out of host memory");
     }
+    const kvq_status s = pages.plan(c, src, dsts, nd);
+    if (s != KVQ_OK) return s;
   }
   thread_local kvq::ForkParams params;  // large tables: one per thread, not on the stack
   kvq::ForkParams& p = params;
@@ -709,6 +745,7 @@ kvq_status enqueue_fork(kvq_cache* c, int src, const int32_t* dsts, int nd, cuda
   p.num_kv_heads = cfg.num_kv_heads;
   p.page_blocks = P;
   p.max_pages = c->max_pages;
+  bool enqueued = false;
   for (int l0 = 0; l0 < cfg.num_layers; l0 += kvq::kForkLayers) {
     p.layers = std::min(kvq::kForkLayers, cfg.num_layers - l0);
     for (int i0 = 0; i0 < nd; i0 += kvq::kForkDsts) {
@@ -737,13 +774,27 @@ kvq_status enqueue_fork(kvq_cache* c, int src, const int32_t* dsts, int nd, cuda
         f.tail_src = 0;
         if (P > 0 && blocks % P != 0) {
           f.tail_src = c->pt_host[at * c->max_pages + f.full_pages];
-          for (int i = 0; i < p.num_dsts; ++i)
-            p.tail_dst[e][i] = c->pt_host[((size_t)(l0 + e) * cfg.max_batch + p.dst[i]) * c->max_pages + f.full_pages];
+          for (int i = 0; i < p.num_dsts; ++i) p.tail_dst[e][i] = pages.tails[(size_t)(l0 + e) * nd + i0 + i];
         }
       }
       const cudaError_t e = kvq::launch_fork(p, stream);
-      if (e != cudaSuccess) return cuda_fail(e, "fork launch");
+      if (e != cudaSuccess) {
+        if (P > 0 && !enqueued) pages.undo(c, dsts, nd);
+        return cuda_fail(e, "fork launch");
+      }
       ++c->launches;
+      if (enqueued) continue;
+      enqueued = true;
+      if (P > 0) pages.commit(c, src, dsts, nd);
+      for (int l = 0; l < cfg.num_layers; ++l) {
+        const size_t base = (size_t)l * cfg.max_batch;
+        for (int i = 0; i < nd; ++i) {
+          c->q_len[base + dsts[i]] = c->q_len[base + src];
+          c->n_len[base + dsts[i]] = c->n_len[base + src];
+          c->s_len[base + dsts[i]] = c->s_len[base + src];
+          c->qv_len[base + dsts[i]] = c->qv_len[base + src];
+        }
+      }
     }
   }
   return KVQ_OK;

@@ -397,6 +397,9 @@ KVQ_API kvq_status kvq_decode_step_window(kvq_cache* cache, int32_t layer, const
  *   that is faster (long prompts or many copies); the result is the same up
  *   to the order of fp32 sums and the roundings (and the limit to 65504) that
  *   kvq_chunk_attention states.
+ * - A launch that fails leaves the cache unchanged; if it is not the call's
+ *   first (over 32 layers or 64 destinations), the destinations hold what
+ *   arrived and are to be forked again or released.
  * No counterpart on the pages: the cache side of parallel sampling.         */
 KVQ_API kvq_status kvq_fork_sequence(kvq_cache* cache, int32_t src, const int32_t* dsts, int32_t num_dsts,
                                      void* stream);

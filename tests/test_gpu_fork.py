@@ -190,3 +190,39 @@ def test_samples_of_a_prompt_decode_together():
                 ref = attend(q[b:b + 1], ck, cv, ck.shape[0] - 1, SCALE, 250, cfg.sink_tokens)[0][0]
                 assert_attention_close(out[b].cpu().numpy(), ref.cpu().numpy(), f"{fmt} sample {b}")
         cache.close()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_a_launch_that_fails_changes_nothing(paged):
+    """On a stream whose capture was invalidated no kernel is enqueued: the call says so, and the lengths and pages
+    are what they were."""
+    cudart = ctypes.CDLL("libcudart.so.12")
+    cache = _paged(pool=30) if paged else make("k2v4_g64", 4, cap=2048, layers=2)
+    cfg = cache.cfg
+    gen = torch.Generator(device="cuda").manual_seed(14)
+    for layer in range(2):
+        k, v, _ = tokens(64 * 13, cfg, gen)
+        cache.append(layer, k, v, [64 * 11, 100, 64 * 2 - 100])
+    cache.fork_sequence(1, [3])
+    before = [[content(cache, layer, b) for b in range(4)] for layer in range(2)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    handle, graph = ctypes.c_void_p(side.cuda_stream), ctypes.c_void_p()
+    assert cudart.cudaStreamBeginCapture(handle, 2) == 0  # relaxed: this stream only
+    try:
+        assert cudart.cudaStreamSynchronize(handle) != 0  # not allowed in a capture, and the end of it
+        n = cache.kernel_launches()
+        with pytest.raises(KvqError) as e:
+            cache.fork_sequence(0, [1, 2, 3], stream=side)
+        assert e.value.status == K.KVQ_ERR_CUDA and cache.kernel_launches() == n
+    finally:
+        cudart.cudaStreamEndCapture(handle, ctypes.byref(graph))
+        cudart.cudaGetLastError()
+    for layer in range(2):
+        for b in range(4):
+            assert same(content(cache, layer, b), before[layer][b]), (layer, b)
+    cache.fork_sequence(0, [1, 2, 3])  # and it works when it can
+    for layer in range(2):
+        for b in (1, 2, 3):
+            assert same(content(cache, layer, b), before[layer][0])
+    cache.close()
