@@ -9,6 +9,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <memory>
 #include <new>
 #include <string>
 #include <vector>
@@ -1085,33 +1086,8 @@ kvq_status enqueue_step(kvq_cache* c, int32_t layer, const void* k, const void* 
 
 }  // namespace
 
-extern "C" {
-
-const char* kvq_status_string(kvq_status s) {
-  switch (s) {
-    case KVQ_OK: return "ok";
-    case KVQ_ERR_INVALID_ARG: return "invalid argument";
-    case KVQ_ERR_UNSUPPORTED: return "unsupported configuration";
-    case KVQ_ERR_CAPACITY: return "sequence capacity exceeded";
-    case KVQ_ERR_WORKSPACE: return "arena or static scratch too small";
-    case KVQ_ERR_CUDA: return "CUDA error";
-  }
-  return "unknown status";
-}
-
-const char* kvq_last_error(void) { return g_last_error.c_str(); }
-
-kvq_status kvq_cache_required_bytes(const kvq_config* cfg, size_t* bytes) {
-  g_last_error.clear();
-  kvq_status s = validate_config(cfg);
-  if (s != KVQ_OK) return s;
-  if (!bytes) return fail(KVQ_ERR_INVALID_ARG, "bytes is null");
-  *bytes = (size_t)make_plan(cfg).total;
-  return KVQ_OK;
-}
-
-kvq_status kvq_cache_create(const kvq_config* cfg, void* dev_arena, size_t arena_bytes, kvq_cache** out) {
-  g_last_error.clear();
+// kvq_cache_create (may throw std::bad_alloc).
+static kvq_status create_cache(const kvq_config* cfg, void* dev_arena, size_t arena_bytes, kvq_cache** out) {
   kvq_status s = validate_config(cfg);
   if (s != KVQ_OK) return s;
   if (!out) return fail(KVQ_ERR_INVALID_ARG, "out is null");
@@ -1120,8 +1096,7 @@ kvq_status kvq_cache_create(const kvq_config* cfg, void* dev_arena, size_t arena
   Plan plan = make_plan(cfg);
   if ((int64_t)arena_bytes < plan.total)
     return fail(KVQ_ERR_WORKSPACE, "arena %zu bytes < required %lld", arena_bytes, (long long)plan.total);
-  kvq_cache* c = new (std::nothrow) kvq_cache;
-  if (!c) return fail(KVQ_ERR_INVALID_ARG, "out of host memory");
+  std::unique_ptr<kvq_cache> c(new kvq_cache);
   c->cfg = *cfg;
   c->k_bits.assign(cfg->k_bits, cfg->k_bits + cfg->num_layers);
   c->v_bits.assign(cfg->v_bits, cfg->v_bits + cfg->num_layers);
@@ -1182,12 +1157,43 @@ kvq_status kvq_cache_create(const kvq_config* cfg, void* dev_arena, size_t arena
       e = cudaMemset(c->arena + c->pt_off[l], 0, (size_t)cfg->max_batch * c->max_pages * 4);
   }
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
-  if (e != cudaSuccess) {
-    delete c;
-    return cuda_fail(e, "zeroing the length table");
-  }
-  *out = c;
+  if (e != cudaSuccess) return cuda_fail(e, "zeroing the length table");
+  *out = c.release();
   return KVQ_OK;
+}
+
+extern "C" {
+
+const char* kvq_status_string(kvq_status s) {
+  switch (s) {
+    case KVQ_OK: return "ok";
+    case KVQ_ERR_INVALID_ARG: return "invalid argument";
+    case KVQ_ERR_UNSUPPORTED: return "unsupported configuration";
+    case KVQ_ERR_CAPACITY: return "sequence capacity exceeded";
+    case KVQ_ERR_WORKSPACE: return "arena or static scratch too small";
+    case KVQ_ERR_CUDA: return "CUDA error";
+  }
+  return "unknown status";
+}
+
+const char* kvq_last_error(void) { return g_last_error.c_str(); }
+
+kvq_status kvq_cache_required_bytes(const kvq_config* cfg, size_t* bytes) {
+  g_last_error.clear();
+  kvq_status s = validate_config(cfg);
+  if (s != KVQ_OK) return s;
+  if (!bytes) return fail(KVQ_ERR_INVALID_ARG, "bytes is null");
+  *bytes = (size_t)make_plan(cfg).total;
+  return KVQ_OK;
+}
+
+kvq_status kvq_cache_create(const kvq_config* cfg, void* dev_arena, size_t arena_bytes, kvq_cache** out) {
+  g_last_error.clear();
+  try {
+    return create_cache(cfg, dev_arena, arena_bytes, out);
+  } catch (const std::bad_alloc&) {
+    return fail(KVQ_ERR_INVALID_ARG, "out of host memory");
+  }
 }
 
 kvq_status kvq_cache_destroy(kvq_cache* c) {

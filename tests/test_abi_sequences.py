@@ -1,6 +1,9 @@
 """Chunk attention, windowed decode and forks without a GPU: what is refused on the host, before any CUDA call."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -68,3 +71,24 @@ def test_integers_wider_than_32_bits_are_refused():
                 cache.decode_step_window: (None, None, None, 5)}[call]
         with pytest.raises(ValueError, match="layer .* 32 bits"):
             call(2 ** 32, *args)
+
+
+def test_a_cache_whose_page_lists_do_not_fit_host_memory_is_refused():
+    """(by a status: a C++ exception must not leave a C entry point)"""
+    code = """
+import ctypes, resource, sys
+import torch
+from asymmetric_bit_kv_b200 import CacheConfig, load_library
+lib = load_library()
+n = 512
+c, keep = CacheConfig(n, 1, 1, 1, 128, 4096, 64, 64, 64, torch.float16, [2] * n, [2] * n, page_blocks=1, pool_pages=1 << 22).to_c()
+h = ctypes.c_void_p()
+used = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (used + (256 << 20),) * 2)
+s = lib.kvq_cache_create(ctypes.byref(c), 0x100000, 1 << 62, ctypes.byref(h))
+print(s, lib.kvq_last_error().decode(), h.value)
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-500:]
+    assert r.stdout.split()[:1] == [str(K.KVQ_ERR_INVALID_ARG)] and "host memory" in r.stdout and r.stdout.strip().endswith("None")
