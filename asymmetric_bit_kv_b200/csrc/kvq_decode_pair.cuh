@@ -109,10 +109,11 @@ __device__ __forceinline__ void pair_prep(const uint8_t* stage, int kc_bytes, co
 // lane (g, t) reads the score of row t / 2 for token g; P.V with column n
 // carrying the probabilities of row n / 4 (every value group of the row gets
 // the same exact product), added to O at the row scale of the value codes.
-// WIN: the chunk's first `skip` tokens are hidden by the window.
+// WIN: the chunk's first `skip` tokens are hidden by the window. Rows from `there`
+// on are no tokens (see ring_chunk).
 template <bool BF16, int VB, bool WIN>
 __device__ __forceinline__ void pair_ring_chunk(const uint8_t* stage, const uint32_t* qw, uint2* bk, int cnt, int skip,
-                                                int NG, int lane, float score_scale, const bool (&valid)[1],
+                                                int there, int NG, int lane, float score_scale, const bool (&valid)[1],
                                                 bool& rq_ready, SoftState<1>& sst, float (&O)[8][4],
                                                 float (&Z)[1][4]) {
   using S = PairShape<VB, 1>;  // value-side constants only
@@ -170,10 +171,9 @@ __device__ __forceinline__ void pair_ring_chunk(const uint8_t* stage, const uint
     const int cch = mt2 / S::MT_PER_CH, P = mt2 % S::MT_PER_CH;
     const int w = (cch * S::CH_SPAN + g * S::VCPC) / 2 + P;
     uint32_t x = V32[(2 * t) * 64 + w], y = V32[(2 * t + 1) * 64 + w];
-    if constexpr (WIN) {  // 0 times what a hidden token holds must not reach the sums
-      if (2 * t < skip) x = 0u;
-      if (2 * t + 1 < skip) y = 0u;
-    }
+    // 0 times what a hidden token or a row that is none holds must not reach the sums
+    if ((WIN && 2 * t < skip) || 2 * t >= there) x = 0u;
+    if ((WIN && 2 * t + 1 < skip) || 2 * t + 1 >= there) y = 0u;
     const uint32_t a[4] = {__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632), 0u, 0u};
     float r[4] = {0.f, 0.f, 0.f, 0.f};
     mma_kv<BF16>(r, a, bh, 0u);
@@ -377,9 +377,9 @@ __global__ void __launch_bounds__(kThreads, 2) decode_pair_kernel(DecodeParams p
         const int cnt = sink ? cnt0 : cnt0 - (p.lag_base - qrow / ngr);
         if (p.new_k && !sink && rc == (p.nres[u.b] - 1) / kResChunk) store_new_token(p, u.b, u.h, nq, stage, lane);
         if (bf16)
-          pair_ring_chunk<true, VB, WIN>(stage, qw, bkw, cnt, skip, NG, lane, p.score_scale, valid, rq_ready, sst, O, Z);
+          pair_ring_chunk<true, VB, WIN>(stage, qw, bkw, cnt, skip, cnt0, NG, lane, p.score_scale, valid, rq_ready, sst, O, Z);
         else
-          pair_ring_chunk<false, VB, WIN>(stage, qw, bkw, cnt, skip, NG, lane, p.score_scale, valid, rq_ready, sst, O, Z);
+          pair_ring_chunk<false, VB, WIN>(stage, qw, bkw, cnt, skip, cnt0, NG, lane, p.score_scale, valid, rq_ready, sst, O, Z);
       }
       __syncwarp();
       if (lane == 0 && n + SPW < nmine) {

@@ -512,10 +512,12 @@ __device__ __forceinline__ void fold_remainders(float (&O)[8][4], float (&Z)[NGR
 // (ch0, ch0+1) from both tokens, paired by one byte permute; two MMAs
 // (probability high and low parts) into a scratch accumulator, added to O at
 // the row scale of the quantized blocks' value codes (2^(p-24)).
-// WIN: the chunk's first `skip` tokens are hidden by the window.
+// WIN: the chunk's first `skip` tokens are hidden by the window. Rows from `there`
+// on are no tokens of the sequence: slots that keep what an older token, or a
+// sequence before this one, left there.
 template <bool BF16, int VB, int NGRP, int NKT, bool WIN>
 __device__ __forceinline__ void ring_chunk(const uint8_t* stage, const uint32_t* qw, uint2* bk,
-                                           const int (&cnt)[heads_per_lane<NKT>()], int skip, int NG,
+                                           const int (&cnt)[heads_per_lane<NKT>()], int skip, int there, int NG,
                                            int lane, float score_scale, const bool (&valid)[heads_per_lane<NKT>()],
                                            bool& rq_ready, SoftState<heads_per_lane<NKT>()>& sst, float (&O)[8][4],
                                            float (&Z)[NGRP][4]) {
@@ -594,10 +596,9 @@ __device__ __forceinline__ void ring_chunk(const uint8_t* stage, const uint32_t*
     const int cch = mt2 / S::MT_PER_CH, P = mt2 % S::MT_PER_CH;
     const int w = (cch * S::CH_SPAN + g * S::VCPC) / 2 + P;
     uint32_t x = V32[(2 * t) * 64 + w], y = V32[(2 * t + 1) * 64 + w];
-    if constexpr (WIN) {  // 0 times what a hidden token holds must not reach the sums
-      if (2 * t < skip) x = 0u;
-      if (2 * t + 1 < skip) y = 0u;
-    }
+    // 0 times what a hidden token or a row that is none holds must not reach the sums
+    if ((WIN && 2 * t < skip) || 2 * t >= there) x = 0u;
+    if ((WIN && 2 * t + 1 < skip) || 2 * t + 1 >= there) y = 0u;
     const uint32_t a[4] = {__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632), 0u, 0u};
     float r[4] = {0.f, 0.f, 0.f, 0.f};
     mma_kv<BF16>(r, a, bh, 0u);
@@ -1201,10 +1202,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_tc_kernel(DecodeParams p, 
             cnt[h] = sink ? cnt0 : cnt0 - (p.lag_base - (HPL == 2 ? 2 * t + h : t) / ngr);
           if (p.new_k && !sink && rc == (p.nres[u.b] - 1) / kResChunk) store_new_token(p, u.b, u.h, nq, stage, lane);
           if (bf16)
-            ring_chunk<true, VB, NGRP, NKT, WIN>(stage, qw, bkw, cnt, skip, NG, lane, p.score_scale, valid, rq_ready,
+            ring_chunk<true, VB, NGRP, NKT, WIN>(stage, qw, bkw, cnt, skip, cnt0, NG, lane, p.score_scale, valid, rq_ready,
                                                  sst, O, Z);
           else
-            ring_chunk<false, VB, NGRP, NKT, WIN>(stage, qw, bkw, cnt, skip, NG, lane, p.score_scale, valid, rq_ready,
+            ring_chunk<false, VB, NGRP, NKT, WIN>(stage, qw, bkw, cnt, skip, cnt0, NG, lane, p.score_scale, valid, rq_ready,
                                                   sst, O, Z);
         }
         // every lane is done with the stage: refill it with item n + SPW
