@@ -226,3 +226,33 @@ def test_a_launch_that_fails_changes_nothing(paged):
         for b in (1, 2, 3):
             assert same(content(cache, layer, b), before[layer][0])
     cache.close()
+
+
+@pytest.mark.parametrize("residual,residual_v", [(192, 64), (64, 256)])
+def test_pages_that_hold_only_keys_or_values_yet(residual, residual_v):
+    """Separate key and value windows in pages: a shared page may hold blocks whose keys (or values) are still in the
+    rings, and every sequence that shares it completes them."""
+    make_one = lambda: KVCache(CacheConfig(1, 4, 8, 2, 128, 4096, 64, 64, residual, torch.bfloat16, [4], [2], residual_v=residual_v,  # noqa: E731
+                                           page_blocks=2, pool_pages=120))
+    cache, twin = make_one(), make_one()
+    cfg = cache.cfg
+    gen = torch.Generator(device="cuda").manual_seed(residual)
+    k, v, _ = tokens(1111, cfg, gen)
+    cache.append(0, k, v, [1111])
+    assert cache.lengths(0, 0)[0] != cache.value_lengths(0, 0)[0]
+    cache.fork_sequence(0, [1, 2, 3])
+    twin.append(0, k.repeat(4, 1, 1), v.repeat(4, 1, 1), [1111] * 4)
+    for lens in ([0, 70, 300, 1], [130, 1, 0, 65], [64, 64, 64, 0]):
+        k, v, q = tokens(sum(lens), cfg, gen)
+        for c in (cache, twin):
+            c.append(0, k, v, lens)
+        q = tokens(4, cfg, gen)[2]
+        for b in range(4):
+            assert same(content(cache, 0, b), content(twin, 0, b)), (lens, b)
+        assert torch.equal(cache.decode_attention(0, q), twin.decode_attention(0, q))
+        assert torch.equal(cache.decode_attention_window(0, q, 300), twin.decode_attention_window(0, q, 300))
+        if lens[0]:
+            cache.release_sequence(0)
+            twin.release_sequence(0)
+    cache.close()
+    twin.close()
