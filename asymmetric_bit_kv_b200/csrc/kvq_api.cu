@@ -574,9 +574,12 @@ kvq_status plan_chunk(const kvq_cache* c, kvq::ChunkParams& p) {
 // an SM processes, 8 us more to rotate and 0.22 per part of a row that is
 // written and merged. Decode of n copies of a prompt of 16 blocks to a page, 32
 // query and 8 KV heads, K2 V4, each on its own / together, in us: 16 x 8200
-// 48 / 61, 32 x 8200 77 / 69, 32 x 32800 226 / 87; 32 KV heads, K2 V2 in groups
-// of 32: 8 x 4000 52 / 61, 16 x 4000 91 / 69, 32 x 8200 294 / 108, 4 x 32800
-// 151 / 157, 32 x 32800 1060 / 198.
+// 47 / 61, 32 x 8200 76 / 69, 8 x 32800 74 / 73, 32 x 32800 231 / 88; 32 KV heads,
+// K2 V2 in groups of 32: 8 x 4000 51 / 61, 16 x 4000 90 / 71, 32 x 8200 299 / 112,
+// 4 x 32800 152 / 175, 32 x 32800 1070 / 217. The 3 ns are those of 2-bit keys:
+// K8 V4 takes 7 (16 x 8200 63 / 55, 32 x 8200 113 / 59, 4 x 32800 61 / 80), so that
+// copies of it stay on their own a little too long, and so do 8 query heads to a
+// KV head (K4 V4, 16 x 8200 76 / 68); 1 does not (32 x 8200 70 / 65).
 bool plan_shared(const kvq_cache* c, int layer, int batch, int32_t slot_cap, kvq::ChunkParams& p,
                  kvq::SharedSlots& slots, int32_t* lo) {
   constexpr double kDecodeTile = 3, kLaunch = 25000, kTile = 2350, kRotate = 8000, kRecord = 0.22;

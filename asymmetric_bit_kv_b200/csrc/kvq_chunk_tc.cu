@@ -47,16 +47,16 @@
 // keep 14 + 6 binary orders below m before they turn subnormal.
 //
 // Measured (one B200; 32 query and 8 KV heads, K2 V4): 4096 new tokens over
-// 32768 in 2555 us, 915 TFLOP/s, 0.56 of the measured rate of large products; a
-// slot's chain (scores, exp2, probabilities, product) bounds it, with the
-// tensor and exp2 pipes at 47% each. 16 x 5 tokens over 8192: 114-120 us, 1.5 us
-// a tile by the same chain (103 with no codes expanded, 112 with half the
-// softmax) and 31 us of launch, start, end and merge. 2 x 300 tokens over 8190,
-// rotated per-token keys: 123 us, of which an item's start and end take a third.
-// Slower: tiles of 64 tokens (2774 us for the first of these), sixteen softmax
-// warps (2705), an issuing warp per slot (2720), the softmax skipped by warps
-// without rows (2893). Where the hot loops fall in the instruction caches moves
-// these figures by 5%.
+// 32768 in 2630 us, 890 TFLOP/s, 0.54 of the measured rate of large products; a
+// slot's chain (scores, exp2, probabilities, product) bounds it, with no pipe
+// above half (tensor and exp2 first). 16 x 5 tokens over 8192: 125 us, 1.5 us a
+// tile by the same chain and 31 us of launch, start, end and merge (at 120 us
+// without expanding codes 103, with half the softmax 112). 2 x 300 tokens over
+// 8190, rotated per-token keys: 126 us, of which an item's start and end take a
+// third. Slower, when the first of these took 2555 to 2618: tiles of 64 tokens
+// (2774), sixteen softmax warps (2705), an issuing warp per slot (2720), the
+// softmax skipped by warps without rows (2893). What the compiler makes of the hot
+// loops moves these figures by 5%, also when code elsewhere in the kernel changes.
 //
 // Every wait is bounded (~2 s): a thread that gives up sets the device error
 // word and an abort flag that ends the others' waits.
@@ -347,8 +347,9 @@ __host__ __device__ inline int code_at(int c, int per) { return per == 4 ? c : (
 __device__ __forceinline__ __half2 limit2(__half2 y) { return __hmin2_nan(y, half2_of(0x7bff7bffu)); }
 // Whether some of a row's codes may: its groups' scales and zero points, each
 // twice in a word. Hardly ever, so that the row is then mended, by a function
-// that stays out of the hot loops: 16 x 5 tokens over 8192 take 119 us (without
-// any of this 120; with the function in line 132, the limit at every pair 138).
+// that stays out of the hot loops: 16 x 5 tokens over 8192 took 119 us with it
+// (without any of this 120; the function in line 132, the limit at every pair
+// 138).
 template <int B>
 __device__ __forceinline__ bool past_fp16(const uint32_t (&s)[2], const uint32_t (&z)[2]) {
   const __half2 top = __float2half2_rn((float)((1 << B) - 1));
@@ -429,9 +430,10 @@ struct Bars {  // shared-memory addresses of arrays of barriers
 // sinks' and a window's first ones of phase B, and the last ones, where each row
 // sees up to its own token. A tile that all rows see needs none of this. Warps 18
 // and 19 look through mixed tiles between their arrival and their use, so that
-// the others' loops stay as they are: 4096 new tokens over 32768 take 2610 us (2570
-// without all of this), 16 x 5 over 8192 126 (119). In the value warps' loop, by
-// calls that hardly ever ran, it cost 2630 to 2800 and 130 to 143.
+// the others' loops stay as they are: 4096 new tokens over 32768 take 2630 us (2570
+// without all of this), 16 x 5 over 8192 125 (119), 4 x 2048 over nothing 217 (208).
+// In the value warps' loop, by calls that hardly ever ran, the first two took 2630
+// to 2800 and 130 to 143.
 struct Lost {
   uint32_t bits[4 * kMixed];
   int any;

@@ -7,8 +7,10 @@
 // destination. A piece is kPiece bytes of one layer's areas laid end to end
 // (key ring, value ring, key sinks, value sinks, then the records head by
 // head); all areas are multiples of 16 bytes, so a 16-byte unit lies in one.
-// Measured: 15 copies, 8 layers (159 MB written) 48 us, 3.3 TB/s; 63 copies, 32
-// layers (2.67 GB) 516 us, 5.2 TB/s; 3 copies, 2 layers 9 us.
+// Measured (8 KV heads): K2 V4, ring of 128 tokens and 14 blocks of 64 in the last
+// page, 15 copies and 8 layers (159 MB written) 48 us, 3.3 TB/s, 63 copies and 32
+// layers (2.67 GB) 516 us, 5.2 TB/s; K4 V2, ring of 64 and no partly filled page, 15
+// copies and 8 layers (31 MB) 14 us; 3 copies, 2 layers 10 us.
 #include <algorithm>
 
 #include "kvq_fork.cuh"
