@@ -63,6 +63,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kvq_chunk.cuh"
 
@@ -72,6 +73,7 @@ namespace {
 
 constexpr int kRows = kChunkSlotRows, kTile = kChunkTile, kD = kHeadDim;
 constexpr int kThreads = 640;
+constexpr int kLaunchRegisters = 96;  // of a thread: what setmaxnreg deals out, 5 x 96 = 144 + 144 + 72 + 72 + 48
 constexpr int kProducers = 128;  // threads of the key warps, and of the value warps
 constexpr int kKStages = 2, kVStages = 2;
 constexpr int kRawStages = 4;           // raw stages at most
@@ -1597,6 +1599,15 @@ bool chunk_tc_supported(const LayerView& L) { return L.residual_v == L.residual;
 
 cudaError_t launch_chunk_tc(const ChunkParams& p, cudaStream_t stream) {
   if (p.items <= 0) return cudaSuccess;
+  // a build whose launch brings fewer registers would wait for them forever
+  static std::atomic<bool> checked{false};
+  if (!checked.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, chunk_tc_kernel);
+    if (e != cudaSuccess) return e;
+    if (a.numRegs < kLaunchRegisters) return cudaErrorLaunchOutOfResources;
+    checked.store(true, std::memory_order_relaxed);
+  }
   ChunkMaps maps;
   cudaError_t e = make_map(maps.k, p, p.k);
   if (e == cudaSuccess) e = make_map(maps.v, p, p.v);

@@ -54,3 +54,14 @@ def test_copies_in_flight_are_waited_for_however_an_item_ends():
     products = products[:products.index("copy_parts(")]
     assert not re.search(r"!issue_products|if \([^)]*\) tc_commit\(bar\.drain\)", products.replace("if (elect_one())", ""))
     assert products.index("tc_commit(bar.drain)") < products.index("mbar_drain(bar.drain, 0)")
+
+
+def test_a_build_with_fewer_registers_is_refused_on_the_host():
+    """A warpgroup that asks for more registers than the block was launched with waits forever: the launcher compares the
+    compiled kernel's count with the shares before its first launch."""
+    kernel, at = _kernel(), SOURCE.index("cudaError_t launch_chunk_tc(")
+    launcher = SOURCE[at:SOURCE.index("chunk_tc_kernel<<<", at)]
+    assert "numRegs" in launcher and "kLaunchRegisters" in launcher
+    shares = [int(n) for n in re.findall(r"setmaxnreg\.\w+\.sync\.aligned\.u32 (\d+);", kernel)]
+    per_group = [shares[0], shares[0], shares[1], shares[1], shares[2]]
+    assert int(re.search(r"kLaunchRegisters = (\d+);", SOURCE)[1]) * len(per_group) >= sum(per_group)
